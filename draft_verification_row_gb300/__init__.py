@@ -12,6 +12,10 @@ from .binding import (  # noqa: F401
     MODES,
     SDVError,
     copy_read_rows,
+    distill_backward,
+    distill_forward,
+    distill_loss,
+    distill_loss_grad,
     gather_read_rows,
     launch_shape,
     lib,
@@ -20,7 +24,10 @@ from .binding import (  # noqa: F401
     lm_head_workspace_bytes,
     read_rows_bytes,
     sample_rows,
+    sample_truncated,
     set_profile_events,
+    top_logits,
+    truncate_rows,
     verify,
     verify_block,
     verify_greedy,

@@ -30,7 +30,9 @@ EXPORTS = list(_ENTRY.values()) + ["sdv_workspace_bytes", "sdv_status_string", "
                                    "sdv_lm_head_workspace_bytes", "sdv_lm_head_logits", "sdv_gather_inner_rows",
                                    "sdv_verify_leaves_apart", "sdv_lm_head_trie_logits", "sdv_verify_residual",
                                    "sdv_verify_multidraft_static", "sdv_testing_set_wait_limit",
-                                   "sdv_testing_verify_without_roots", "sdv_testing_set_lm_head_single_cta"]
+                                   "sdv_testing_verify_without_roots", "sdv_testing_set_lm_head_single_cta",
+                                   "sdv_sample_truncated", "sdv_truncate_rows", "sdv_top_logits",
+                                   "sdv_distill_forward", "sdv_distill_backward", "sdv_distill_loss_grad"]
 
 
 class SDVError(RuntimeError):
@@ -98,6 +100,22 @@ def lib(path: str = LIB_PATH):
     h.sdv_read_rows_bytes.restype = ctypes.c_int
     h.sdv_read_rows_bytes.argtypes = ([ctypes.c_int] * 4 + [ctypes.c_longlong, ctypes.c_int] + [ctypes.c_void_p] * 2
                                       + [ctypes.POINTER(ctypes.c_longlong)])
+    settings = [ctypes.c_float, ctypes.c_int, ctypes.c_float, ctypes.c_float] + [ctypes.c_void_p] * 4
+    rows = [ctypes.c_int, ctypes.c_int, ctypes.c_longlong, ctypes.c_int]
+    h.sdv_sample_truncated.restype = ctypes.c_int
+    h.sdv_sample_truncated.argtypes = rows + settings + [ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 4
+    h.sdv_truncate_rows.restype = ctypes.c_int
+    h.sdv_truncate_rows.argtypes = rows + settings + [ctypes.c_void_p] * 2 + [ctypes.c_longlong] + [ctypes.c_void_p] * 2
+    h.sdv_top_logits.restype = ctypes.c_int
+    h.sdv_top_logits.argtypes = rows + [ctypes.c_float, ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 5
+    record = [ctypes.c_float, ctypes.c_void_p, ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 4
+    h.sdv_distill_forward.restype = ctypes.c_int
+    h.sdv_distill_forward.argtypes = rows + record + [ctypes.c_void_p] * 4
+    h.sdv_distill_backward.restype = ctypes.c_int
+    h.sdv_distill_backward.argtypes = rows + record + [ctypes.c_void_p] * 3 + [ctypes.c_longlong, ctypes.c_void_p]
+    h.sdv_distill_loss_grad.restype = ctypes.c_int
+    h.sdv_distill_loss_grad.argtypes = (rows + record + [ctypes.c_void_p] * 2 + [ctypes.c_longlong]
+                                        + [ctypes.c_void_p] * 2)
     _lib = h
     return h
 
@@ -272,6 +290,249 @@ def sample_rows(logits, n_samples, u, temperature, *, V=None, tokens=None, devic
         raise SDVError(rc, "sdv_sample_rows")
     return tokens, device_status
 
+
+def _rows(name, t, V):
+    """(n_rows, V, row stride) of a CUDA [n_rows][width] tensor with contiguous rows."""
+    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA [n_rows][width] tensor with contiguous rows")
+    n, width = t.shape
+    V = width if V is None else int(V)
+    if V > width:
+        raise ValueError(f"{name} has fewer than V = {V} columns")
+    stride = t.stride(0) if n > 1 else width
+    if stride < V:
+        raise ValueError(f"{name}'s rows overlap")
+    return n, V, stride
+
+
+def _vector(name, t, n, dtype, device):
+    """A contiguous [n] array on the rows' device, or None."""
+    if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous() or tuple(t.shape) != (n,)):
+        raise ValueError(f"{name} must be a contiguous {dtype} [n_rows] tensor on the rows' device")
+    return t
+
+
+def _c_int(name, x):
+    if not -2**31 <= int(x) < 2**31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return int(x)
+
+
+def _settings(n, device, temperature, top_k, top_p, min_p):
+    """The common settings and the rows' arrays of a truncated distribution: each is a number or an [n_rows] tensor."""
+    common, arrays = [], []
+    for name, x, cast, dtype in (("temperature", temperature, float, torch.float32), ("top_k", top_k, int, torch.int32),
+                                 ("top_p", top_p, float, torch.float32), ("min_p", min_p, float, torch.float32)):
+        if torch.is_tensor(x):
+            arrays.append(_vector(name, x, n, dtype, device))
+            common.append(cast(1 if name == "top_p" else 0))
+        else:
+            arrays.append(None)
+            common.append(cast(x) if cast is float else _c_int(name, x))
+    return common, arrays
+
+
+def _status(device_status, device):
+    if device_status is None:
+        return torch.empty(1, dtype=torch.int32, device=device)
+    return _vector("device_status", device_status, 1, torch.int32, device)
+
+
+def _stream(stream, device):
+    return ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+
+
+def sample_truncated(logits, n_samples, u, temperature, *, top_k=0, top_p=1.0, min_p=0.0, V=None, tokens=None,
+                     device_status=None, stream=None):
+    """n_samples draws per row of softmax(logits / T) truncated by top-k, top-p and min-p (sdv_sample_truncated).
+
+    logits [n_rows][width] (float32 or bfloat16, CUDA; each row contiguous, any row stride), u [n_rows][n_samples]
+    float32 (may be None when temperature is the number 0).  temperature, top_k (int32), top_p and min_p are numbers
+    or [n_rows] CUDA tensors, one setting per row; top_k = 0, top_p = 1 and min_p = 0 leave a truncation out.  Returns
+    (tokens [n_rows][n_samples] int32, device_status [1] int32); the call is asynchronous.
+    """
+    h = lib()
+    n, V, stride = _rows("logits", logits, V)
+    n_samples = _c_int("n_samples", n_samples)
+    if n_samples < 1:
+        raise ValueError("n_samples must be at least 1")
+    if u is not None and (u.dtype != torch.float32 or u.device != logits.device or not u.is_contiguous()
+                          or tuple(u.shape) != (n, n_samples)):
+        raise ValueError("u must be a contiguous CUDA float32 [n_rows][n_samples] tensor")
+    common, arrays = _settings(n, logits.device, temperature, top_k, top_p, min_p)
+    if tokens is None:
+        tokens = torch.empty((n, n_samples), dtype=torch.int32, device=logits.device)
+    elif (tokens.dtype != torch.int32 or tokens.device != logits.device or not tokens.is_contiguous()
+          or tuple(tokens.shape) != (n, n_samples)):
+        raise ValueError("tokens must be a contiguous CUDA int32 [n_rows][n_samples] tensor")
+    device_status = _status(device_status, logits.device)
+    rc = h.sdv_sample_truncated(n, V, stride, _dtype_code(logits), *common, *map(_ptr, arrays), _ptr(logits), n_samples,
+                                _ptr(u), _ptr(tokens), _ptr(device_status), _stream(stream, logits.device))
+    if rc != 0:
+        raise SDVError(rc, "sdv_sample_truncated")
+    return tokens, device_status
+
+
+def truncate_rows(logits, temperature, *, top_k=0, top_p=1.0, min_p=0.0, V=None, out=None, device_status=None,
+                  stream=None):
+    """The rows with every token outside the truncated distribution at -inf (sdv_truncate_rows): what verification
+    under top-k, top-p and min-p reads.
+
+    logits and the settings as in sample_truncated.  out: a tensor of the same type and at least V columns (logits
+    itself: in place); columns past V are not written.  Without it, a new contiguous [n_rows][V] tensor.  Returns (out,
+    device_status); the call is asynchronous.
+    """
+    h = lib()
+    n, V, stride = _rows("logits", logits, V)
+    common, arrays = _settings(n, logits.device, temperature, top_k, top_p, min_p)
+    if out is None:
+        out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+    n_out, _, out_stride = _rows("out", out, V)
+    if n_out != n or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError("out must have the logits' rows, type and device")
+    device_status = _status(device_status, logits.device)
+    rc = h.sdv_truncate_rows(n, V, stride, _dtype_code(logits), *common, *map(_ptr, arrays), _ptr(logits), _ptr(out),
+                             out_stride, _ptr(device_status), _stream(stream, logits.device))
+    if rc != 0:
+        raise SDVError(rc, "sdv_truncate_rows")
+    return out, device_status
+
+
+def top_logits(logits, k, temperature=1.0, *, V=None, device_status=None, stream=None):
+    """The k largest logits of each row in descending order, their tokens, and the log-sum-exp of the others at
+    temperature T (sdv_top_logits): a teacher's record for distill_loss.
+
+    Returns (values [n_rows][k] of the logits' type, index [n_rows][k] int32, rest [n_rows] float32, device_status);
+    the call is asynchronous.
+    """
+    h = lib()
+    n, V, stride = _rows("logits", logits, V)
+    k, dev = _c_int("k", k), logits.device
+    if k < 1:
+        raise ValueError("k must be at least 1")
+    values = torch.empty((n, k), dtype=logits.dtype, device=dev)
+    index = torch.empty((n, k), dtype=torch.int32, device=dev)
+    rest = torch.empty(n, dtype=torch.float32, device=dev)
+    device_status = _status(device_status, dev)
+    rc = h.sdv_top_logits(n, V, stride, _dtype_code(logits), float(temperature), _ptr(logits), k, _ptr(values),
+                          _ptr(index), _ptr(rest), _ptr(device_status), _stream(stream, dev))
+    if rc != 0:
+        raise SDVError(rc, "sdv_top_logits")
+    return values, index, rest, device_status
+
+
+def _record(student, values, index, rest, row_weight, V):
+    n, V, stride = _rows("student", student, V)
+    dev = student.device
+    if (values.dim() != 2 or values.shape[0] != n or values.device != dev or not values.is_contiguous()):
+        raise ValueError("values must be a contiguous [n_rows][k] tensor on the student's device")
+    if (index.dtype != torch.int32 or index.shape != values.shape or index.device != dev or not index.is_contiguous()):
+        raise ValueError("index must be a contiguous int32 tensor of values' shape")
+    _vector("rest", rest, n, torch.float32, dev)
+    _vector("row_weight", row_weight, n, torch.float32, dev)
+    return n, V, stride
+
+
+def distill_forward(student, values, index, rest=None, *, temperature=1.0, row_weight=None, V=None, stats=None,
+                    device_status=None, stream=None):
+    """The distillation loss of each row (sdv_distill_forward); stats: a [n_rows][4] float32 tensor to be written for
+    distill_backward, or None.  Returns (loss [n_rows] float32, device_status)."""
+    h = lib()
+    n, V, stride = _record(student, values, index, rest, row_weight, V)
+    loss = torch.empty(n, dtype=torch.float32, device=student.device)
+    if stats is not None and (stats.dtype != torch.float32 or tuple(stats.shape) != (n, 4)
+                              or not stats.is_contiguous() or stats.device != student.device):
+        raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
+    device_status = _status(device_status, student.device)
+    rc = h.sdv_distill_forward(n, V, stride, _dtype_code(student), float(temperature), _ptr(student), values.shape[1],
+                               _dtype_code(values), _ptr(values), _ptr(index), _ptr(rest), _ptr(row_weight),
+                               _ptr(loss), _ptr(stats), _ptr(device_status), _stream(stream, student.device))
+    if rc != 0:
+        raise SDVError(rc, "sdv_distill_forward")
+    return loss, device_status
+
+
+def _grad_rows(student, grad, n, V):
+    if grad is None:
+        # columns past V, where there are any, have no gradient
+        shape = student.shape
+        grad = (torch.empty if V == shape[1] else torch.zeros)(shape, dtype=student.dtype, device=student.device)
+    n_grad, _, stride = _rows("grad", grad, V)
+    if n_grad != n or grad.dtype != student.dtype or grad.device != student.device:
+        raise ValueError("grad must have the student's rows, type and device")
+    return grad, stride
+
+
+def distill_backward(student, values, index, rest, stats, grad_loss=None, *, temperature=1.0, row_weight=None, V=None,
+                     grad=None, stream=None):
+    """The gradient of sum_r grad_loss[r] loss[r] with respect to the student's logits (sdv_distill_backward), from
+    distill_forward's inputs and stats.  Returns grad, of the student's type."""
+    h = lib()
+    n, V, stride = _record(student, values, index, rest, row_weight, V)
+    if (stats.dtype != torch.float32 or tuple(stats.shape) != (n, 4) or not stats.is_contiguous()
+            or stats.device != student.device):
+        raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
+    _vector("grad_loss", grad_loss, n, torch.float32, student.device)
+    grad, grad_stride = _grad_rows(student, grad, n, V)
+    rc = h.sdv_distill_backward(n, V, stride, _dtype_code(student), float(temperature), _ptr(student), values.shape[1],
+                                _dtype_code(values), _ptr(values), _ptr(index), _ptr(rest), _ptr(row_weight),
+                                _ptr(stats), _ptr(grad_loss), _ptr(grad), grad_stride,
+                                _stream(stream, student.device))
+    if rc != 0:
+        raise SDVError(rc, "sdv_distill_backward")
+    return grad
+
+
+def distill_loss_grad(student, values, index, rest=None, *, temperature=1.0, row_weight=None, V=None, grad=None,
+                      device_status=None, stream=None):
+    """Loss and gradient of its sum in one call (sdv_distill_loss_grad): for a step that knows its rows' weights
+    beforehand (grad: student itself writes the gradient in place).  Returns (loss [n_rows] float32, grad of the
+    student's type, device_status)."""
+    h = lib()
+    n, V, stride = _record(student, values, index, rest, row_weight, V)
+    loss = torch.empty(n, dtype=torch.float32, device=student.device)
+    grad, grad_stride = _grad_rows(student, grad, n, V)
+    device_status = _status(device_status, student.device)
+    rc = h.sdv_distill_loss_grad(n, V, stride, _dtype_code(student), float(temperature), _ptr(student),
+                                 values.shape[1], _dtype_code(values), _ptr(values), _ptr(index), _ptr(rest),
+                                 _ptr(row_weight), _ptr(loss), _ptr(grad), grad_stride, _ptr(device_status),
+                                 _stream(stream, student.device))
+    if rc != 0:
+        raise SDVError(rc, "sdv_distill_loss_grad")
+    return loss, grad, device_status
+
+
+class _DistillLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, student, values, index, rest, row_weight, temperature, V):
+        stats = None
+        if ctx.needs_input_grad[0]:
+            stats = torch.empty((student.shape[0], 4), dtype=torch.float32, device=student.device)
+            ctx.save_for_backward(student, values, index, rest, row_weight, stats)
+            ctx.settings = dict(temperature=temperature, V=V)
+        return distill_forward(student, values, index, rest, temperature=temperature, row_weight=row_weight, V=V,
+                               stats=stats)[0]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss):
+        student, values, index, rest, row_weight, stats = ctx.saved_tensors
+        grad = distill_backward(student, values, index, rest, stats, grad_loss.float().contiguous(),
+                                row_weight=row_weight, **ctx.settings)
+        return (grad,) + (None,) * 6
+
+
+def distill_loss(student, values, index, rest=None, *, temperature=1.0, row_weight=None, V=None):
+    """Distillation loss of each row against a teacher's record (top_logits), differentiable with respect to the
+    student's logits.
+
+    student [n_rows][width] (float32 or bfloat16, contiguous rows), values [n_rows][k] (float32 or bfloat16), index
+    [n_rows][k] int32 (below 0: absent), rest [n_rows] float32 or None (the teacher renormalised over its k tokens),
+    row_weight [n_rows] float32 or None.  Returns loss [n_rows] float32:
+    row_weight * KL(teacher || student) over the record's tokens and one outcome for all others, at temperature T.
+    The teacher's record and the weights get no gradient.
+    """
+    return _DistillLoss.apply(student, values, index, rest, row_weight, float(temperature), V)
 
 
 def _bf16_rows(name, t, d=None):

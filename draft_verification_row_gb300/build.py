@@ -12,9 +12,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsdv.so")
-SOURCES = ["sdv_api.cu", "sdv_kernels.cu", "sdv_stream.cu", "sdv_sample.cu", "sdv_static.cu", "sdv_lmhead.cu"]
+SOURCES = ["sdv_api.cu", "sdv_kernels.cu", "sdv_stream.cu", "sdv_sample.cu", "sdv_static.cu", "sdv_lmhead.cu",
+           "sdv_truncate.cu", "sdv_top.cu", "sdv_distill.cu"]
 HEADERS = [os.path.join(ROOT, "include", "sdv.h"), os.path.join(CSRC, "sdv_internal.h"),
-           os.path.join(CSRC, "sdv_device.cuh")]
+           os.path.join(CSRC, "sdv_device.cuh"), os.path.join(CSRC, "sdv_rows.cuh")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 

@@ -567,6 +567,220 @@ int sdv_sample_rows(int n_rows, int V, long long row_stride, int dtype, float te
     return sdv::launch_sample_rows(a, st) == cudaSuccess ? SDV_OK : SDV_ERR_CUDA;
 }
 
+// Rows of the whole-row operators: any stride, aligned to their type.
+static bool row_args_ok(int n_rows, int V, long long row_stride, int dtype)
+{
+    return n_rows >= 0 && V >= 1 && V <= SDV_MAX_V && (dtype == SDV_F32 || dtype == SDV_BF16) && row_stride >= V &&
+           row_stride <= (1ll << 40);
+}
+
+static size_t elem_bytes(int dtype) { return dtype == SDV_F32 ? 4 : 2; }
+
+// A required device array, aligned to its elements.
+static bool array_ok(const void* p, size_t elem) { return p && sdv::aligned(p, elem) && sdv::device_accessible(p); }
+
+static bool array_or_null_ok(const void* p, size_t elem) { return !p || array_ok(p, elem); }
+
+// log2(e) / T for T > 0; infinite or NaN where it cannot be used.
+static double scale_of(float temperature)
+{
+    return temperature > 0.f ? 1.4426950408889634 / (double)temperature : NAN;
+}
+
+static int truncated(const sdv::TruncArgs& a, void* cuda_stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    if (!row_args_ok(a.n_rows, a.V, a.stride, a.dtype)) return SDV_ERR_INVALID;
+    if (!a.row_temperature && !(a.temperature == 0.f || (std::isfinite(a.temperature) &&
+                                                         std::isfinite((float)scale_of(a.temperature)))))
+        return SDV_ERR_INVALID;
+    if (!a.row_top_k && a.top_k < 0) return SDV_ERR_INVALID;
+    if (!a.row_top_p && !(a.top_p > 0.f && a.top_p <= 1.f)) return SDV_ERR_INVALID;
+    if (!a.row_min_p && !(a.min_p >= 0.f && a.min_p <= 1.f)) return SDV_ERR_INVALID;
+    if (!array_or_null_ok(a.device_status, 4)) return SDV_ERR_INVALID;
+    if (a.n_rows > 0) {
+        if (!array_ok(a.logits, elem_bytes(a.dtype))) return SDV_ERR_INVALID;
+        if (a.out ? !array_ok(a.out, elem_bytes(a.dtype)) || a.out_stride < a.V ||
+                        (a.out == a.logits && a.out_stride != a.stride)
+                  : !array_ok(a.tokens, 4) ||
+                        ((a.row_temperature || a.temperature > 0.f || a.u) && !array_ok(a.u, 4)))
+            return SDV_ERR_INVALID;
+        if (!array_or_null_ok(a.row_temperature, 4) || !array_or_null_ok(a.row_top_k, 4) ||
+            !array_or_null_ok(a.row_top_p, 4) || !array_or_null_ok(a.row_min_p, 4))
+            return SDV_ERR_INVALID;
+    }
+    if (a.device_status && cudaMemsetAsync(a.device_status, 0, sizeof(int), st) != cudaSuccess) return SDV_ERR_CUDA;
+    if (a.n_rows == 0) return SDV_OK;
+    return sdv::launch_truncate(a, st) == cudaSuccess ? SDV_OK : SDV_ERR_CUDA;
+}
+
+static sdv::TruncArgs trunc_args(int n_rows, int V, long long row_stride, int dtype, float temperature, int top_k,
+                                 float top_p, float min_p, const float* row_temperature, const int* row_top_k,
+                                 const float* row_top_p, const float* row_min_p, const void* logits,
+                                 int* device_status)
+{
+    sdv::TruncArgs a = {};
+    a.n_rows = n_rows;
+    a.V = V;
+    a.dtype = dtype;
+    a.stride = row_stride;
+    a.logits = logits;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.row_temperature = row_temperature;
+    a.row_top_k = row_top_k;
+    a.row_top_p = row_top_p;
+    a.row_min_p = row_min_p;
+    a.device_status = device_status;
+    return a;
+}
+
+int sdv_sample_truncated(int n_rows, int V, long long row_stride, int dtype, float temperature, int top_k,
+                         float top_p, float min_p, const float* row_temperature, const int* row_top_k,
+                         const float* row_top_p, const float* row_min_p, const void* logits, int n_samples,
+                         const float* u, int* tokens, int* device_status, void* cuda_stream)
+{
+    if (n_samples < 1 || n_samples > SDV_MAX_SAMPLES) return SDV_ERR_INVALID;
+    sdv::TruncArgs a = trunc_args(n_rows, V, row_stride, dtype, temperature, top_k, top_p, min_p, row_temperature,
+                                  row_top_k, row_top_p, row_min_p, logits, device_status);
+    a.n_samples = n_samples;
+    a.u = u;
+    a.tokens = tokens;
+    return truncated(a, cuda_stream);
+}
+
+int sdv_truncate_rows(int n_rows, int V, long long row_stride, int dtype, float temperature, int top_k, float top_p,
+                      float min_p, const float* row_temperature, const int* row_top_k, const float* row_top_p,
+                      const float* row_min_p, const void* logits, void* out, long long out_stride,
+                      int* device_status, void* cuda_stream)
+{
+    if (n_rows > 0 && !out) return SDV_ERR_INVALID;
+    if (out_stride < V || out_stride > (1ll << 40)) return SDV_ERR_INVALID;
+    sdv::TruncArgs a = trunc_args(n_rows, V, row_stride, dtype, temperature, top_k, top_p, min_p, row_temperature,
+                                  row_top_k, row_top_p, row_min_p, logits, device_status);
+    a.out = out;
+    a.out_stride = out_stride;
+    return truncated(a, cuda_stream);
+}
+
+int sdv_top_logits(int n_rows, int V, long long row_stride, int dtype, float temperature, const void* logits, int k,
+                   void* values, int* index, float* rest, int* device_status, void* cuda_stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    if (!row_args_ok(n_rows, V, row_stride, dtype) || k < 1 || k > SDV_MAX_TOP) return SDV_ERR_INVALID;
+    sdv::TopArgs a;
+    a.c = scale_of(temperature);
+    if (!std::isfinite(temperature) || !std::isfinite((float)a.c)) return SDV_ERR_INVALID;
+    if (!array_or_null_ok(device_status, 4)) return SDV_ERR_INVALID;
+    const size_t e = elem_bytes(dtype);
+    if (n_rows > 0 && (!array_ok(logits, e) || !array_ok(values, e) || !array_ok(index, 4) || !array_ok(rest, 4)))
+        return SDV_ERR_INVALID;
+    if (device_status && cudaMemsetAsync(device_status, 0, sizeof(int), st) != cudaSuccess) return SDV_ERR_CUDA;
+    if (n_rows == 0) return SDV_OK;
+    a.n_rows = n_rows;
+    a.V = V;
+    a.dtype = dtype;
+    a.k = k;
+    a.stride = row_stride;
+    a.inv_T = 1.0 / (double)temperature;
+    a.logits = logits;
+    a.values = values;
+    a.index = index;
+    a.rest = rest;
+    a.device_status = device_status;
+    return sdv::launch_top(a, st) == cudaSuccess ? SDV_OK : SDV_ERR_CUDA;
+}
+
+static int distill(sdv::DistillArgs& a, float temperature, bool forward, bool backward, void* cuda_stream)
+{
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    if (!row_args_ok(a.n_rows, a.V, a.stride, a.dtype) || a.k < 0 || a.k > SDV_MAX_TOP) return SDV_ERR_INVALID;
+    if (a.teacher_dtype != SDV_F32 && a.teacher_dtype != SDV_BF16) return SDV_ERR_INVALID;
+    const double c = scale_of(temperature);
+    if (!std::isfinite(temperature) || !std::isfinite((float)c)) return SDV_ERR_INVALID;
+    if (backward && (a.grad_stride < a.V || a.grad_stride > (1ll << 40))) return SDV_ERR_INVALID;
+    if (!array_or_null_ok(a.device_status, 4)) return SDV_ERR_INVALID;
+    if (a.n_rows > 0) {
+        const size_t e = elem_bytes(a.dtype);
+        if (!array_ok(a.student, e)) return SDV_ERR_INVALID;
+        if (a.k > 0 && (!array_ok(a.values, elem_bytes(a.teacher_dtype)) || !array_ok(a.index, 4)))
+            return SDV_ERR_INVALID;
+        if (!array_or_null_ok(a.rest, 4) || !array_or_null_ok(a.row_weight, 4) || !array_or_null_ok(a.grad_loss, 4) ||
+            !array_or_null_ok(a.stats, 4))
+            return SDV_ERR_INVALID;
+        if (forward && !array_ok(a.loss, 4)) return SDV_ERR_INVALID;
+        if (backward && (!array_ok(a.grad, e) || (a.grad == a.student && a.grad_stride != a.stride)))
+            return SDV_ERR_INVALID;
+        if (!forward && !a.stats) return SDV_ERR_INVALID;
+    }
+    if (a.device_status && cudaMemsetAsync(a.device_status, 0, sizeof(int), st) != cudaSuccess) return SDV_ERR_CUDA;
+    if (a.n_rows == 0) return SDV_OK;
+    a.c = (float)c;
+    a.inv_T = (float)(1.0 / (double)temperature);
+    return sdv::launch_distill(a, st) == cudaSuccess ? SDV_OK : SDV_ERR_CUDA;
+}
+
+static sdv::DistillArgs distill_args(int n_rows, int V, long long row_stride, int dtype, const void* student, int k,
+                                     int teacher_dtype, const void* values, const int* index, const float* rest,
+                                     const float* row_weight)
+{
+    sdv::DistillArgs a = {};
+    a.n_rows = n_rows;
+    a.V = V;
+    a.stride = row_stride;
+    a.dtype = dtype;
+    a.student = student;
+    a.k = k;
+    a.teacher_dtype = teacher_dtype;
+    a.values = values;
+    a.index = index;
+    a.rest = rest;
+    a.row_weight = row_weight;
+    return a;
+}
+
+int sdv_distill_forward(int n_rows, int V, long long row_stride, int dtype, float temperature, const void* student,
+                        int k, int teacher_dtype, const void* values, const int* index, const float* rest,
+                        const float* row_weight, float* loss, float* stats, int* device_status, void* cuda_stream)
+{
+    sdv::DistillArgs a = distill_args(n_rows, V, row_stride, dtype, student, k, teacher_dtype, values, index, rest,
+                                      row_weight);
+    a.loss = loss;
+    a.stats = stats;
+    a.device_status = device_status;
+    return distill(a, temperature, true, false, cuda_stream);
+}
+
+int sdv_distill_backward(int n_rows, int V, long long row_stride, int dtype, float temperature, const void* student,
+                         int k, int teacher_dtype, const void* values, const int* index, const float* rest,
+                         const float* row_weight, const float* stats, const float* grad_loss, void* grad,
+                         long long grad_stride, void* cuda_stream)
+{
+    sdv::DistillArgs a = distill_args(n_rows, V, row_stride, dtype, student, k, teacher_dtype, values, index, rest,
+                                      row_weight);
+    a.stats = const_cast<float*>(stats);
+    a.grad_loss = grad_loss;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    return distill(a, temperature, false, true, cuda_stream);
+}
+
+int sdv_distill_loss_grad(int n_rows, int V, long long row_stride, int dtype, float temperature, const void* student,
+                          int k, int teacher_dtype, const void* values, const int* index, const float* rest,
+                          const float* row_weight, float* loss, void* grad, long long grad_stride,
+                          int* device_status, void* cuda_stream)
+{
+    sdv::DistillArgs a = distill_args(n_rows, V, row_stride, dtype, student, k, teacher_dtype, values, index, rest,
+                                      row_weight);
+    a.loss = loss;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    a.device_status = device_status;
+    return distill(a, temperature, true, true, cuda_stream);
+}
+
 int sdv_launch_shape(int V, int dtype, int* ctas_per_sm, int* threads, int* smem_bytes)
 {
     if (V < 1 || V > SDV_MAX_V || (dtype != SDV_F32 && dtype != SDV_BF16)) return SDV_ERR_INVALID;

@@ -1,0 +1,304 @@
+// sdv_distill.cu -- the distillation loss of a draft model against a
+// teacher's top logits, and its gradient.
+//
+// The outcomes of a row are the teacher's k tokens and one for all other
+// tokens: p = softmax(t_1/T .. t_k/T, rest) with the teacher's record
+// (rest: the log-sum-exp of its other logits, -inf where it is not given),
+// q_j = e_j / Z and q_r = O / Z with e_i = exp(s_i/T - max), O the sum of
+// the other tokens' e_i and Z = O + sum_j e_j.
+//   loss = w (sum_j p_j ln(p_j / q_j) + p_r ln(p_r / q_r))
+//   d loss / d s_i = (w g / T) (q_i - p_i)             a teacher's token
+//                    (w g / T) q_i (1 - p_r / q_r)     any other
+// (the derivative of -sum p ln q, where sum p = 1).  O is summed directly
+// from the other tokens, never as Z minus the rest: where the k tokens
+// hold nearly all of the mass, that difference has no digits left.
+//
+// One CTA per row.  The teacher's tokens are marked in a bitmap in shared
+// memory, which the pass over the row asks a byte at a time.  The gradient
+// is a second pass, which reads the row (from L2 where the first pass was
+// of the same call) and writes every element as another token's; the k
+// tokens' elements are written over after a barrier.
+#include "sdv_internal.h"
+#include "sdv_rows.cuh"
+
+namespace sdv {
+namespace {
+
+template <int NT>
+struct DistillSmem {
+    float part[NT / 32];
+    int bad;
+    float p[SDV_MAX_TOP];    // teacher's probabilities
+    float s[SDV_MAX_TOP];    // the student's logits at its tokens
+    int index[SDV_MAX_TOP];  // tokens, -1: absent
+};
+
+// The marks of unit u's elements (bit e: element e is a teacher's token).
+template <int DT>
+__device__ __forceinline__ uint32_t marks_of(const uint32_t* bitmap, int u)
+{
+    // the bitmap is laid out by unit position (off + index)
+    return DT == SDV_F32 ? bitmap[u >> 3] >> (u & 7) * 4 & 0xfu : bitmap[u >> 2] >> (u & 3) * 8 & 0xffu;
+}
+
+template <int NT>
+__device__ float block_sum_f(float v, float* part)
+{
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) t += part[i];
+    return t;
+}
+
+template <int NT>
+__device__ float block_max_f(float v, float* part)
+{
+    v = warp_max_redux(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = part[0];
+#pragma unroll
+    for (int i = 1; i < NT / 32; ++i) t = max_nan(t, part[i]);
+    return t;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// One unit of a gradient row: as 16 bytes where it is whole and aligned,
+// else by elements.
+template <int DT>
+__device__ __forceinline__ void store_unit(const Row& g, bool alike, const Row& row, int u,
+                                           const float (&v)[Elem<DT>::kPerUnit])
+{
+    constexpr int EPU = Elem<DT>::kPerUnit;
+    if (alike && whole_unit<DT>(row, u)) {
+        uint4 w;
+        if (DT == SDV_F32)
+            w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else
+            w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4 % EPU], v[5 % EPU]),
+                           pack_bf16(v[6 % EPU], v[7 % EPU]));
+        reinterpret_cast<uint4*>(g.p)[u] = w;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < EPU; ++e) {
+        const int x = u * EPU + e - row.off;
+        if (x < 0 || x >= row.V) continue;
+        if (DT == SDV_F32)
+            reinterpret_cast<float*>(g.p)[x + g.off] = v[e];
+        else
+            reinterpret_cast<unsigned short*>(g.p)[x + g.off] = (unsigned short)pack_bf16(v[e], 0.f);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_elem(const Row& g, int x, float v)
+{
+    if (DT == SDV_F32)
+        reinterpret_cast<float*>(g.p)[x + g.off] = v;
+    else
+        reinterpret_cast<unsigned short*>(g.p)[x + g.off] = (unsigned short)pack_bf16(v, 0.f);
+}
+
+template <int DT, int NT>
+__device__ void fill_row(const Row& g, float x)
+{
+    float v[Elem<DT>::kPerUnit];
+#pragma unroll
+    for (int e = 0; e < Elem<DT>::kPerUnit; ++e) v[e] = x;
+    for (int u = threadIdx.x; u < g.n_units; u += NT) store_unit<DT>(g, true, g, u, v);
+}
+
+// What a call computes: the loss (with the row's statistics for a later
+// backward call), the gradient from those statistics, or loss and gradient.
+enum { DISTILL_FORWARD = 0, DISTILL_BACKWARD = 1, DISTILL_BOTH = 2 };
+
+template <int DT, int NT, int MODE>
+__global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a)
+{
+    constexpr int EPU = Elem<DT>::kPerUnit;
+    constexpr bool kStats = MODE != DISTILL_BACKWARD, kGrad = MODE != DISTILL_FORWARD;
+    __shared__ DistillSmem<NT> sm;
+    extern __shared__ uint32_t bitmap[];
+    const int r = blockIdx.x, tid = threadIdx.x;
+    const Row row = row_at<DT>(a.student, r, a.stride, a.V);
+    const Row grow = kGrad ? row_at<DT>(a.grad, r, a.grad_stride, a.V) : row;
+    float* const stats = a.stats ? a.stats + (size_t)r * 4 : nullptr;
+    const float weight = a.row_weight ? a.row_weight[r] : 1.f;
+    if (weight == 0.f) {  // a masked row is not looked at
+        if (kGrad) fill_row<DT, NT>(grow, 0.f);
+        if (kStats && tid == 0) {
+            a.loss[r] = 0.f;
+            if (stats) stats[0] = stats[1] = stats[2] = stats[3] = 0.f;
+        }
+        return;
+    }
+    // the teacher's record and the student's logits at its tokens
+    const int k = a.k;
+    if (kStats)
+        for (int i = tid; i < (row.n_units * EPU + 31) / 32; i += NT) bitmap[i] = 0u;
+    if (tid == 0) sm.bad = 0;
+    __syncthreads();
+    const float rest = a.rest ? a.rest[r] : -INFINITY;
+    float tm = rest;  // already divided by T, as every teacher value below
+    float M = -INFINITY;
+    for (int j = tid; j < k; j += NT) {
+        const size_t o = (size_t)r * k + j;
+        int x = a.index[o];
+        float t = a.teacher_dtype == SDV_F32
+                      ? static_cast<const float*>(a.values)[o]
+                      : __uint_as_float((uint32_t) static_cast<const unsigned short*>(a.values)[o] << 16);
+        t = x < 0 ? -INFINITY : t * a.inv_T;
+        float s = -INFINITY;
+        if (x >= a.V) {
+            atomicOr(&sm.bad, SDV_REQ_BAD_TOKEN);
+            x = -1;
+        } else if (x >= 0) {
+            const int bit = x + row.off;
+            if (kStats && (atomicOr(&bitmap[bit >> 5], 1u << (bit & 31)) >> (bit & 31) & 1u))
+                atomicOr(&sm.bad, SDV_REQ_BAD_TOKEN);  // a token named twice
+            s = load_elem<DT>(row, x);
+        }
+        sm.index[j] = x < 0 ? -1 : x;
+        sm.p[j] = t;
+        sm.s[j] = s;
+        tm = max_nan(tm, t);
+        M = max_nan(M, s);
+    }
+    tm = block_max_f<NT>(tm, sm.part);  // a barrier: bitmap, bad and the record are there
+    // the student's statistics: mo the largest of its other tokens, zo their
+    // sum against mo, M the row's maximum, Z its sum against M
+    float mo, zo, Z;
+    if (kStats) {
+        float m = -INFINITY, z = 0.f;  // this thread's: its maximum so far, the sum against it
+        for (int u = tid; u < row.n_units; u += NT) {
+            float v[EPU];
+            load_elems<DT>(row, u, v);
+            const uint32_t marks = marks_of<DT>(bitmap, u);
+            float cm = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) {
+                if (marks >> e & 1u) v[e] = -INFINITY;
+                cm = max_nan(cm, v[e]);
+            }
+            if (!(cm <= m)) {
+                z = m > -INFINITY ? z * ex2((m - cm) * a.c) : 0.f;
+                m = cm;
+            }
+            if (m > -INFINITY) {
+#pragma unroll
+                for (int e = 0; e < EPU; ++e) z += ex2((v[e] - m) * a.c);
+            }
+        }
+        mo = block_max_f<NT>(m, sm.part);
+        M = block_max_f<NT>(max_nan(M, mo), sm.part);
+        // NaN, +Inf or nothing finite, or a bad token: loss and gradient are NaN
+        const bool finite = M > -INFINITY && M < INFINITY;
+        if (!finite || sm.bad) {
+            if (kGrad) fill_row<DT, NT>(grow, NAN);
+            if (tid == 0) {
+                a.loss[r] = NAN;
+                if (stats) stats[0] = stats[1] = stats[2] = stats[3] = NAN;
+                if (a.device_status) atomicOr(a.device_status, (finite ? 0 : SDV_REQ_NONFINITE) | sm.bad);
+            }
+            return;
+        }
+        zo = block_sum_f<NT>(m > -INFINITY ? z * ex2((m - mo) * a.c) : 0.f, sm.part);
+        float zs = 0.f;
+        for (int j = tid; j < k; j += NT) zs += sm.s[j] > -INFINITY ? ex2((sm.s[j] - M) * a.c) : 0.f;
+        Z = block_sum_f<NT>(zs, sm.part) + (mo > -INFINITY ? zo * ex2((mo - M) * a.c) : 0.f);
+        if (stats && tid == 0) {
+            stats[0] = mo;
+            stats[1] = zo;
+            stats[2] = M;
+            stats[3] = Z;
+        }
+    } else {
+        mo = stats[0];
+        zo = stats[1];
+        M = stats[2];
+        Z = stats[3];
+        if (!(M < INFINITY) || sm.bad) {  // the forward call found the row unusable
+            fill_row<DT, NT>(grow, NAN);
+            return;
+        }
+    }
+    // the teacher's probabilities
+    const bool taught = !(tm == -INFINITY);  // false: the record is empty, nothing is learnt from the row
+    float zt = 0.f;
+    for (int j = tid; j < k; j += NT) zt += expf(sm.p[j] - tm);
+    zt = block_sum_f<NT>(zt, sm.part) + expf(rest - tm);
+    const float lzt = logf(zt);
+    const float lpr = (rest - tm) - lzt, pr = expf(lpr);
+    const float lz = logf(Z);
+    float loss = 0.f;
+    for (int j = tid; j < k; j += NT) {
+        const float lp = (sm.p[j] - tm) - lzt, p = expf(lp);
+        if (kStats && !(p == 0.f)) loss += p * (lp - ((sm.s[j] - M) * a.inv_T - lz));
+        sm.p[j] = p;
+    }
+    if (kStats) {
+        loss = block_sum_f<NT>(loss, sm.part);
+        if (!(pr == 0.f)) loss += pr * (lpr - ((mo - M) * a.inv_T + logf(zo) - lz));
+        if (tid == 0) a.loss[r] = taught ? weight * loss : 0.f;
+    }
+    if (!kGrad) return;
+    if (!taught) {
+        fill_row<DT, NT>(grow, 0.f);
+        return;
+    }
+    const float scale = weight * (a.grad_loss ? a.grad_loss[r] : 1.f) * a.inv_T;
+    // another token: scale (q_i - p_r q_i / q_r), both against mo, so that
+    // neither factor is lost where the k tokens hold nearly all of the mass
+    const float fo = mo > -INFINITY ? scale * (ex2((mo - M) * a.c) / Z - pr / zo) : 0.f;
+    const float ref = mo > -INFINITY ? mo : 0.f;
+    const bool alike = grow.off == row.off;
+    for (int u = tid; u < row.n_units; u += NT) {
+        float v[EPU];
+        load_elems<DT>(row, u, v);
+#pragma unroll
+        for (int e = 0; e < EPU; ++e) v[e] = fo * ex2((v[e] - ref) * a.c);
+        store_unit<DT>(grow, alike, row, u, v);
+    }
+    __syncthreads();  // the teacher's tokens are written over
+    for (int j = tid; j < k; j += NT) {
+        const int x = sm.index[j];
+        if (x >= 0) store_elem<DT>(grow, x, scale * (ex2((sm.s[j] - M) * a.c) / Z - sm.p[j]));
+    }
+}
+
+template <int DT, int MODE>
+cudaError_t launch(const DistillArgs& a, cudaStream_t st)
+{
+    // the bitmap, by element position from the row's first 16-byte boundary
+    const size_t smem = MODE == DISTILL_BACKWARD ? 0 : ((size_t)a.V + 2 * Elem<DT>::kPerUnit + 31) / 32 * 4;
+    distill_kernel<DT, 512, MODE><<<a.n_rows, 512, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t launch(const DistillArgs& a, cudaStream_t st)
+{
+    if (!a.grad) return launch<DT, DISTILL_FORWARD>(a, st);
+    return a.loss ? launch<DT, DISTILL_BOTH>(a, st) : launch<DT, DISTILL_BACKWARD>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_distill(const DistillArgs& a, cudaStream_t st)
+{
+    return a.dtype == SDV_F32 ? launch<SDV_F32>(a, st) : launch<SDV_BF16>(a, st);
+}
+
+}  // namespace sdv

@@ -96,6 +96,62 @@ struct SampleArgs {
     int* device_status;
 };
 cudaError_t launch_sample_rows(const SampleArgs& a, cudaStream_t st);
+
+// Truncated sampling and truncated rows (sdv_truncate.cu).
+struct TruncArgs {
+    int n_rows, V, dtype;
+    long long stride;
+    const void* logits;
+    float temperature;  // the settings of every row, where the row's array is NULL
+    int top_k;
+    float top_p, min_p;
+    const float* row_temperature;  // [n_rows] each, or NULL
+    const int* row_top_k;
+    const float* row_top_p;
+    const float* row_min_p;
+    int n_samples;
+    const float* u;  // [n_rows][n_samples]
+    int* tokens;     // [n_rows][n_samples], or NULL: no draws
+    void* out;       // [n_rows][out_stride], or NULL: no rows
+    long long out_stride;
+    int* device_status;
+};
+cudaError_t launch_truncate(const TruncArgs& a, cudaStream_t st);
+
+// A teacher's top logits (sdv_top.cu).
+struct TopArgs {
+    int n_rows, V, dtype, k;
+    long long stride;
+    double c;       // log2(e) / T
+    double inv_T;
+    const void* logits;
+    void* values;   // [n_rows][k]
+    int* index;     // [n_rows][k]
+    float* rest;    // [n_rows]
+    int* device_status;
+};
+cudaError_t launch_top(const TopArgs& a, cudaStream_t st);
+
+// The distillation loss and its gradient (sdv_distill.cu).
+struct DistillArgs {
+    int n_rows, V, dtype, k, teacher_dtype;
+    long long stride;
+    float c;      // log2(e) / T
+    float inv_T;
+    const void* student;
+    const void* values;      // [n_rows][k]
+    const int* index;        // [n_rows][k]
+    const float* rest;       // [n_rows] or NULL
+    const float* row_weight; // [n_rows] or NULL
+    const float* grad_loss;  // [n_rows] or NULL (1)
+    float* loss;             // [n_rows]; NULL: backward (stats are read)
+    float* stats;            // [n_rows][4]: {mo, zo, M, Z}; forward: written, or NULL
+    void* grad;              // [n_rows][grad_stride]; NULL: forward
+    long long grad_stride;
+    int* device_status;
+};
+cudaError_t launch_distill(const DistillArgs& a, cudaStream_t st);
+
 // Per request: the decision, then the correction (or bonus) draw at its end
 // node (sdv_sample.cu).
 // after_nodes: launched right after the node kernel, as its programmatic

@@ -1,0 +1,355 @@
+// sdv_rows.cuh -- device helpers of the whole-row operators (truncated
+// sampling, truncated rows, top logits, distillation): rows of any
+// alignment read as 16-byte units, an order-preserving integer key of a
+// logit, exact fixed-point weights, block-wide sums and scans, and the
+// search for the border of a prefix of the row's descending order.
+#pragma once
+
+#include "sdv_device.cuh"
+
+namespace sdv {
+namespace {
+
+typedef unsigned long long u64;
+
+// ------------------------------------------------------------------------
+// rows as 16-byte units
+
+// A row of V elements whose first one need not lie on a 16-byte boundary:
+// unit u holds the elements u * kPerUnit - off .. + kPerUnit - 1, and those
+// outside 0..V-1 read as -inf (no mass, never the maximum, never kept).
+struct Row {
+    char* p;  // the row's first element, rounded down to 16 bytes
+    int off;  // elements before it in its first unit
+    int V;
+    int n_units;
+};
+
+template <int DT>
+__device__ __forceinline__ Row row_at(const void* base, long long r, long long stride, int V)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(base) + (uintptr_t)(r * stride * Elem<DT>::kBytes);
+    Row row;
+    row.p = reinterpret_cast<char*>(a & ~(uintptr_t)15);
+    row.off = (int)(a & 15) / Elem<DT>::kBytes;
+    row.V = V;
+    row.n_units = (row.off + V + Elem<DT>::kPerUnit - 1) / Elem<DT>::kPerUnit;
+    return row;
+}
+
+template <int DT>
+__device__ __forceinline__ bool whole_unit(const Row& row, int u)
+{
+    const int x0 = u * Elem<DT>::kPerUnit - row.off;
+    return x0 >= 0 && x0 + Elem<DT>::kPerUnit <= row.V;
+}
+
+// A unit that the row's first or last element falls into: element by
+// element, so that nothing outside the row is read.
+template <int DT>
+__device__ __noinline__ uint4 edge_unit(const Row& row, int u)
+{
+    constexpr int EPU = Elem<DT>::kPerUnit;
+    uint32_t w[4];
+    const int x0 = u * EPU - row.off;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (DT == SDV_F32) {
+            const int x = x0 + i;
+            w[i] = x >= 0 && x < row.V ? reinterpret_cast<const uint32_t*>(row.p)[(size_t)u * 4 + i] : 0xff800000u;
+        } else {
+            const unsigned short* h = reinterpret_cast<const unsigned short*>(row.p) + (size_t)u * 8 + 2 * i;
+            const int x = x0 + 2 * i;
+            const uint32_t lo = x >= 0 && x < row.V ? h[0] : 0xff80u;
+            const uint32_t hi = x + 1 >= 0 && x + 1 < row.V ? h[1] : 0xff80u;
+            w[i] = lo | hi << 16;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 load_unit(const Row& row, int u)
+{
+    if (whole_unit<DT>(row, u)) return reinterpret_cast<const uint4*>(row.p)[u];
+    return edge_unit<DT>(row, u);
+}
+
+template <int DT>
+__device__ __forceinline__ void load_elems(const Row& row, int u, float (&v)[Elem<DT>::kPerUnit])
+{
+    Elem<DT>::unpack(load_unit<DT>(row, u), v);
+}
+
+template <int DT>
+__device__ __forceinline__ float load_elem(const Row& row, int x)
+{
+    const size_t i = (size_t)x + row.off;
+    if (DT == SDV_F32) return reinterpret_cast<const float*>(row.p)[i];
+    return __uint_as_float((uint32_t) reinterpret_cast<const unsigned short*>(row.p)[i] << 16);
+}
+
+// ------------------------------------------------------------------------
+// keys: unsigned integers in the order of the logits (-0 and +0 alike).  A
+// bf16 logit has a 16-bit key, so that keys next to each other are logits
+// next to each other.
+
+template <int DT>
+__device__ __forceinline__ uint32_t key_of(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.f);  // -0 + 0 is +0
+    const uint32_t k = b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+    return DT == SDV_F32 ? k : k >> 16;
+}
+
+template <int DT>
+__device__ __forceinline__ float key_value(uint32_t key)
+{
+    if (DT == SDV_F32) return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+    const uint32_t h = key & 0x8000u ? key ^ 0x8000u : ~key & 0xffffu;
+    return __uint_as_float(h << 16);
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t lowest_finite_key()
+{
+    return DT == SDV_F32 ? 0x00800000u : 0x0080u;
+}
+
+// ------------------------------------------------------------------------
+// fixed-point weights
+
+// 2^(j / 64) in units of 2^-62.
+__device__ const u64 kExp2Table[64] = {
+    0x4000000000000000ull, 0x40b268f9de0183baull, 0x4166c34c5615d0ecull, 0x421d1461d66f2023ull,
+    0x42d561b3e6243d8aull, 0x438fb0cb4f468808ull, 0x444c0740496d4294ull, 0x450a6abaa4b77ecdull,
+    0x45cae0f1f545eb73ull, 0x468d6fadbf2dd4f3ull, 0x47521cc5a2e6a9e0ull, 0x4818ee218a3358eeull,
+    0x48e1e9b9d588e19bull, 0x49ad159789f37496ull, 0x4a7a77d47f7b84b1ull, 0x4b4a169b900c2d00ull,
+    0x4c1bf828c6dc54b8ull, 0x4cf022c9905bfd32ull, 0x4dc69cdceaa72a9cull, 0x4e9f6cd3967fdba8ull,
+    0x4f7a993048d088d7ull, 0x50582887dcb8a7e1ull, 0x513821818624b40cull, 0x521a8ad704f3404full,
+    0x52ff6b54d8a89c75ull, 0x53e6c9da74b29ab5ull, 0x54d0ad5a753e077cull, 0x55bd1cdad49f699cull,
+    0x56ac1f752150a563ull, 0x579dbc56b48521baull, 0x5891fac0e95612c8ull, 0x5988e20954889245ull,
+    0x5a827999fcef3242ull, 0x5b7ec8f19468bbc9ull, 0x5c7dd7a3b17dcf75ull, 0x5d7fad59099f22feull,
+    0x5e8451cfac061b5full, 0x5f8bccdb3d398841ull, 0x6096266533384a2bull, 0x61a3666d124bb204ull,
+    0x62b39508aa836d6full, 0x63c6ba6455dcd8aeull, 0x64dcdec3371793d1ull, 0x65f60a7f79393e2eull,
+    0x6712460a8fc24072ull, 0x683199ed779592caull, 0x69540ec8f895722dull, 0x6a79ad55e7f6fd10ull,
+    0x6ba27e656b4eb57aull, 0x6cce8ae13c57ebdbull, 0x6dfddbcbed791babull, 0x6f307a412f074892ull,
+    0x70666f76154a7089ull, 0x719fc4b95f452d29ull, 0x72dc8373be41a454ull, 0x741cb5281e25ee34ull,
+    0x75606373ee921c97ull, 0x76a7980f6cca15c2ull, 0x77f25ccdee6d7ae6ull, 0x7940bb9e2cffd89dull,
+    0x7a92be8a92436616ull, 0x7be86fb985689ddcull, 0x7d41d96db915019dull, 0x7e9f06067a4360baull,
+};
+
+constexpr int kWeightBits = 45;
+constexpr int kWeightSpan = kWeightBits + 1;  // 2^-46 and below round to 0
+
+// The weight exp((x - M) / T) of a logit x <= M as an integer multiple of
+// 2^-45, with a relative error of about 2^-39: sums of integers do not
+// depend on their order, and 2^18 weights (the longest row) stay below 2^63.
+// A border of the kept set and a draw's crossing are then settled as 64-bit
+// arithmetic settles them, except where a sum lies within about 1e-12 of
+// them.  fp32 sums (1e-7) would move the border of a nucleus whose last
+// tokens have a mass of 1e-5 in one row of a hundred.
+//   y = (x - M) c with c = log2(e) / T held in two floats; the difference
+//   and the product are exact pairs.  y = n / 64 + r with |r| <= 1/128,
+//   2^y = 2^(n >> 6) table[n & 63] (1 + (2^r - 1)), and 2^r - 1 by its
+//   series, the linear term in two floats.  About 45 instructions, none of
+//   them fp64 (whose rate on this GPU is 1/64 of fp32's).
+struct Scale {
+    float ch, cl;  // log2(e) / T = ch + cl
+    float M;       // the row's maximum
+};
+
+__device__ __forceinline__ u64 weight_of(float x, const Scale& s, const u64* table)
+{
+    const float dh = __fsub_rn(x, s.M);
+    const float yh = __fmul_rn(dh, s.ch);
+    if (!(yh >= -(float)kWeightSpan)) return 0;
+    const float bb = __fsub_rn(dh, x);
+    const float dl = __fadd_rn(__fsub_rn(x, __fsub_rn(dh, bb)), __fsub_rn(-s.M, bb));
+    const float yl = __fadd_rn(__fmaf_rn(dh, s.ch, -yh), __fmaf_rn(dh, s.cl, __fmul_rn(dl, s.ch)));
+    const float nf = rintf(yh * 64.f);
+    const float r0 = __fmaf_rn(nf, -1.f / 64.f, yh);
+    const float rh = __fadd_rn(r0, yl);
+    const float rl = __fsub_rn(yl, __fsub_rn(rh, r0));
+    constexpr float kLn2 = 0.693147182f, kLn2Lo = -1.90465421e-9f;
+    const float t = __fmul_rn(rh, kLn2);
+    float lo = __fadd_rn(__fmaf_rn(rh, kLn2, -t), __fmaf_rn(rh, kLn2Lo, __fmul_rn(rl, kLn2)));
+    const float p = fmaf(rh, fmaf(rh, fmaf(rh, 0.00133335581f, 0.00961812911f), 0.0555041087f), 0.240226507f);
+    lo = fmaf(rh * rh, p, lo);
+    constexpr float kUnit = 1125899906842624.f;  // 2^50
+    const long long f = __float2ll_rn(t * kUnit) + __float2ll_rn(lo * kUnit);
+    const int n = (int)nf;
+    const u64 e = table[n & 63];
+    const u64 w = e + (u64)__mul64hi((long long)e, f << 14);
+    const int shift = 62 - kWeightBits - (n >> 6);  // 17 .. 63
+    return (w + (1ull << (shift - 1))) >> shift;
+}
+
+// ------------------------------------------------------------------------
+// block-wide sums and scans (NT threads, all of them)
+
+template <int NT>
+struct BlockSmem {
+    u64 part[NT / 32];
+    u64 total;
+    u64 base;    // find_border: amount before the border's bucket
+    int bucket;  // find_border: the border's bucket, or -1
+};
+
+__device__ __forceinline__ u64 warp_sum_u64(u64 v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ u64 warp_scan_u64(u64 v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 n = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += n;
+    }
+    return v;
+}
+
+template <int NT>
+__device__ u64 block_sum(u64 v, BlockSmem<NT>& s)
+{
+    v = warp_sum_u64(v);
+    __syncthreads();  // the last reader of part
+    if ((threadIdx.x & 31) == 0) s.part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    u64 t = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) t += s.part[i];
+    return t;
+}
+
+// Sum over the threads before this one; total: over all of them.
+template <int NT>
+__device__ u64 block_scan(u64 v, u64& total, BlockSmem<NT>& s)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const u64 incl = warp_scan_u64(v, lane);
+    __syncthreads();
+    if (lane == 31) s.part[w] = incl;
+    __syncthreads();
+    u64 before = 0, t = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        const u64 p = s.part[i];
+        if (i < w) before += p;
+        t += p;
+    }
+    total = t;
+    return before + incl - v;
+}
+
+template <int NT>
+__device__ float block_max_nan(float v, BlockSmem<NT>& s)
+{
+    v = warp_max_redux(v);
+    float* part = reinterpret_cast<float*>(s.part);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float m = part[0];
+#pragma unroll
+    for (int i = 1; i < NT / 32; ++i) m = max_nan(m, part[i]);
+    return m;
+}
+
+// ------------------------------------------------------------------------
+// the border of a prefix of the descending order
+
+constexpr int kBuckets = 1024;
+
+struct Hist {
+    uint32_t lo[kBuckets], hi[kBuckets];
+};
+
+struct Border {
+    uint32_t key;  // the key at which the prefix sum reaches `need`
+    u64 above;     // the sum over all larger keys
+    bool found;    // false: the whole sum is below `need`
+};
+
+// Where the sum over elements in descending order of their keys reaches
+// need (> 0): of 1 for each element, or of its weight (mass).  Elements
+// with keys in klo..khi count.  The range is cut into 1024 buckets of equal
+// width, whose sums are taken with shared-memory atomics on 32-bit words
+// (integers: the order does not matter; a weight's carry goes from the low
+// word to the high one), and the bucket of the border is cut again until
+// it is one key: at most four passes over the source for 32-bit keys, two
+// for 16-bit ones.  src.each(f) calls f(x) for each of this thread's
+// elements.
+template <int DT, int NT, class Src>
+__device__ Border find_border(const Src& src, bool mass, u64 need, uint32_t klo, uint32_t khi, const Scale& sc,
+                              const u64* table, Hist& h, BlockSmem<NT>& bs)
+{
+    constexpr int kPer = kBuckets / NT;
+    static_assert(kBuckets % NT == 0, "buckets per thread");
+    const int tid = threadIdx.x;
+    Border b;
+    b.above = 0;
+    b.found = true;
+    for (;;) {
+        const uint32_t span = khi - klo;
+        const int bits = 32 - __clz((int)span);
+        const int shift = bits > 10 ? bits - 10 : 0;
+        __syncthreads();
+        for (int i = tid; i < kBuckets; i += NT) h.lo[i] = h.hi[i] = 0u;
+        if (tid == 0) bs.bucket = -1;
+        __syncthreads();
+        src.each([&](float x) {
+            const uint32_t k = key_of<DT>(x);
+            if (k < klo || k > khi) return;
+            const uint32_t i = (khi - k) >> shift;
+            if (mass) {
+                const u64 w = weight_of(x, sc, table);
+                const uint32_t lo = (uint32_t)w;
+                const uint32_t old = atomicAdd(&h.lo[i], lo);
+                const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
+                if (hi) atomicAdd(&h.hi[i], hi);
+            } else {
+                atomicAdd(&h.lo[i], 1u);
+            }
+        });
+        __syncthreads();
+        u64 v[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            v[i] = (u64)h.hi[tid * kPer + i] << 32 | h.lo[tid * kPer + i];
+            sum += v[i];
+        }
+        u64 total;
+        u64 run = b.above + block_scan<NT>(sum, total, bs);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (run < need && run + v[i] >= need) {
+                bs.bucket = tid * kPer + i;
+                bs.base = run;
+            }
+            run += v[i];
+        }
+        __syncthreads();
+        if (bs.bucket < 0) {
+            b.key = klo;
+            b.above += total;
+            b.found = false;
+            return b;
+        }
+        b.above = bs.base;
+        khi -= (uint32_t)bs.bucket << shift;
+        const uint32_t width = (1u << shift) - 1u;
+        klo = khi - klo > width ? khi - width : klo;
+        if (shift == 0) {
+            b.key = khi;
+            return b;
+        }
+    }
+}
+
+}  // namespace
+}  // namespace sdv

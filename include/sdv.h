@@ -94,6 +94,7 @@ extern "C" {
 #define SDV_MAX_L 16      /* draft tokens per draft */
 #define SDV_MAX_V 262144  /* vocabulary size */
 #define SDV_MAX_SAMPLES 64 /* draws per row in sdv_sample_rows */
+#define SDV_MAX_TOP 1024   /* logits of a teacher's record */
 
 /* logit element types */
 enum { SDV_F32 = 0, SDV_BF16 = 1 };
@@ -116,7 +117,8 @@ enum {
     SDV_REQ_BAD_LENGTH = 1, /* lengths[b] outside 0..L */
     SDV_REQ_BAD_TOKEN = 2,  /* a used draft token outside [0, V) */
     SDV_REQ_NONFINITE = 4,  /* a used row holds NaN or +Inf, or no finite value */
-    SDV_DEV_TIMEOUT = 8     /* a bounded device wait gave up; outputs are not valid */
+    SDV_DEV_TIMEOUT = 8,    /* a bounded device wait gave up; outputs are not valid */
+    SDV_REQ_BAD_SETTING = 16 /* a row's temperature, top_k, top_p or min_p is out of range */
 };
 
 /*
@@ -237,6 +239,129 @@ const char *sdv_status_string(int status);
  * neighbouring token. */
 int sdv_sample_rows(int n_rows, int V, long long row_stride, int dtype, float temperature, const void *logits,
                     int n_samples, const float *u, int *tokens, int *device_status, void *cuda_stream);
+
+/* ---------------------------------------------------------------------------
+ * Truncated distributions: temperature, top-k, top-p and min-p.
+ *
+ * Servers draw from truncated distributions, and speculative decoding is
+ * exact only if the rules see the distributions that the drafts were drawn
+ * from and the target is to be sampled from.  sdv_sample_truncated draws
+ * tokens; sdv_truncate_rows writes the same truncation as logits, -inf
+ * outside the kept set, for the sdv_verify_* calls and sdv_sample_rows.
+ *
+ * Of a row's tokens in descending order of their logits (ties: lowest index
+ * first), with weights w_i = exp((x_i - max) / T):
+ *   n_k  the first top_k tokens (0: all); Z_k their weights' sum;
+ *   n_p  the fewest first tokens whose weights sum to at least top_p Z_k
+ *        (1: all n_k);
+ *   n_m  the tokens with w_i >= min_p (0: all).
+ * The first max(1, min(n_k, n_p, n_m)) are kept; tokens whose logit is -inf
+ * never are.  T = 0 keeps the row's argmax, lowest index on ties.
+ * Sums are fixed-point integers with steps of 2^-45 of the largest weight:
+ * the results do not depend on the order of summation, and agree with
+ * 64-bit arithmetic except where a sum lies within about 1e-12 (relative)
+ * of its border.
+ *   n_rows, V, dtype  as in sdv_sample_rows.
+ *   row_stride   elements between rows, >= V; any value.
+ *   temperature, top_k, top_p, min_p  every row's settings: T >= 0 with
+ *                1 / T finite; top_k >= 0; 0 < top_p <= 1; 0 <= min_p <= 1.
+ *   row_temperature, row_top_k, row_top_p, row_min_p  [n_rows] device
+ *                arrays (fp32, int32, fp32, fp32) or NULL: where given,
+ *                used instead of the common value (which is then ignored).
+ *                A row whose setting is out of range is unusable.
+ *   logits       [n_rows][row_stride] device memory, aligned to its type;
+ *                columns >= V are never read.
+ *   device_status [1] device int32 or NULL: zeroed, then the OR of
+ *                SDV_REQ_NONFINITE (a row holding NaN or +Inf, or no finite
+ *                logit) and SDV_REQ_BAD_SETTING.  Other rows are unaffected.
+ *   cuda_stream  the stream to run on (NULL: the default stream).
+ * Asynchronous; nothing is allocated.  Return SDV_OK, SDV_ERR_INVALID or
+ * SDV_ERR_CUDA. */
+
+/* n_samples draws per row from the kept tokens: the first token in index
+ * order whose running sum of kept weights exceeds u times their sum.
+ *   n_samples    1..SDV_MAX_SAMPLES.
+ *   u            [n_rows][n_samples] device fp32 uniforms in [0, 1); may be
+ *                NULL when row_temperature is NULL and temperature is 0.
+ *   tokens       [n_rows][n_samples] device int32 out; -1 in unusable rows. */
+int sdv_sample_truncated(int n_rows, int V, long long row_stride, int dtype, float temperature, int top_k,
+                         float top_p, float min_p, const float *row_temperature, const int *row_top_k,
+                         const float *row_top_p, const float *row_min_p, const void *logits, int n_samples,
+                         const float *u, int *tokens, int *device_status, void *cuda_stream);
+
+/* The rows with every token that is not kept at -inf; unusable rows are
+ * copied as they are.
+ *   out          [n_rows][out_stride] device memory of the same dtype,
+ *                aligned to it; out_stride >= V; columns >= V are not
+ *                written.  May be logits itself with the same stride (in
+ *                place); otherwise the two must not overlap. */
+int sdv_truncate_rows(int n_rows, int V, long long row_stride, int dtype, float temperature, int top_k, float top_p,
+                      float min_p, const float *row_temperature, const int *row_top_k, const float *row_top_p,
+                      const float *row_min_p, const void *logits, void *out, long long out_stride,
+                      int *device_status, void *cuda_stream);
+
+/* ---------------------------------------------------------------------------
+ * Training a draft model on the target's rows.
+ *
+ * sdv_top_logits takes from each row (the teacher's) its k largest logits in
+ * descending order (ties: lowest index first), their tokens, and
+ * rest = ln sum over all other tokens of exp(x_i / T).
+ *   k            1..SDV_MAX_TOP.
+ *   temperature  T > 0 with 1 / T finite.
+ *   values       [n_rows][k] of dtype, index [n_rows][k] int32, rest
+ *                [n_rows] fp32, device memory, out.  Tokens whose logit is
+ *                -inf are not listed: entries past the last finite logit
+ *                have value -inf and index -1; rest is -inf where no other
+ *                finite logit is left.  An unusable row gets values and rest
+ *                NaN and indices -1.
+ *   The other arguments are as above. */
+int sdv_top_logits(int n_rows, int V, long long row_stride, int dtype, float temperature, const void *logits, int k,
+                   void *values, int *index, float *rest, int *device_status, void *cuda_stream);
+
+/* The distillation loss of draft logits s against such records, and its
+ * gradient.  Outcomes: the record's tokens, and one for all other tokens.
+ *   p = softmax(values_1 / T, .., values_k / T, rest)
+ *   q_j = exp(s_j / T) / sum_i exp(s_i / T) of the record's tokens, and q_r
+ *   of all others together
+ *   loss = weight (sum_j p_j ln(p_j / q_j) + p_r ln(p_r / q_r))
+ *   d loss / d s_i = weight / T (q_i - p_i)            a record's token
+ *                    weight / T q_i (1 - p_r / q_r)    any other
+ * (a term with p = 0 is 0).
+ *   student      [n_rows][row_stride] of dtype, device memory, aligned to
+ *                its type; row_stride >= V, any value.
+ *   k            0..SDV_MAX_TOP; teacher_dtype the type of values.
+ *   values, index  [n_rows][k]; an index below 0 is an absent entry (its
+ *                value is not used).  A row's indices are distinct and below
+ *                V, else its loss and gradient are NaN (SDV_REQ_BAD_TOKEN).
+ *   rest         [n_rows] fp32, or NULL: -inf for every row (the teacher is
+ *                renormalised over its k tokens).  A row without any teacher
+ *                mass has loss and gradient 0.
+ *   row_weight   [n_rows] fp32 or NULL (1).  A row of weight 0 has loss 0
+ *                and gradient 0, and nothing else of it is read.
+ *   loss         [n_rows] fp32 out.  NaN, +Inf or no finite logit in a row:
+ *                its loss and gradient are NaN (SDV_REQ_NONFINITE).
+ *   stats        [n_rows][4] fp32, written by sdv_distill_forward (or NULL)
+ *                for sdv_distill_backward on the same inputs.
+ *   grad_loss    [n_rows] fp32 or NULL (1): the derivative of what is
+ *                minimised with respect to each row's loss.
+ *   grad         [n_rows][grad_stride] of dtype, out; grad_stride >= V.  May
+ *                be student itself with the same stride (in place);
+ *                otherwise the two must not overlap.
+ * sdv_distill_loss_grad is forward and backward (with grad_loss 1) in one
+ * call that reads each row from HBM once: for a training step that knows its
+ * rows' weights beforehand.  Sums and exponentials are fp32.  Asynchronous;
+ * nothing is allocated.  Return SDV_OK, SDV_ERR_INVALID or SDV_ERR_CUDA. */
+int sdv_distill_forward(int n_rows, int V, long long row_stride, int dtype, float temperature, const void *student,
+                        int k, int teacher_dtype, const void *values, const int *index, const float *rest,
+                        const float *row_weight, float *loss, float *stats, int *device_status, void *cuda_stream);
+int sdv_distill_backward(int n_rows, int V, long long row_stride, int dtype, float temperature, const void *student,
+                         int k, int teacher_dtype, const void *values, const int *index, const float *rest,
+                         const float *row_weight, const float *stats, const float *grad_loss, void *grad,
+                         long long grad_stride, void *cuda_stream);
+int sdv_distill_loss_grad(int n_rows, int V, long long row_stride, int dtype, float temperature, const void *student,
+                          int k, int teacher_dtype, const void *values, const int *index, const float *rest,
+                          const float *row_weight, float *loss, void *grad, long long grad_stride,
+                          int *device_status, void *cuda_stream);
 
 /* Launch shape of the node kernel (the one that reads vocabulary rows) for
  * rows of V elements of dtype: CTAs per SM (it is persistent: that many
