@@ -124,13 +124,82 @@ __device__ void fill_row(const Row& g, float x)
 // backward call), the gradient from those statistics, or loss and gradient.
 enum { DISTILL_FORWARD = 0, DISTILL_BACKWARD = 1, DISTILL_BOTH = 2 };
 
-template <int DT, int NT, int MODE>
-__global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a)
+// The sum of 2^(x c - e) over one unit against the exponent e.
+template <int DT>
+__device__ __forceinline__ float unit_sum(const uint4& raw, float c, float e)
 {
     constexpr int EPU = Elem<DT>::kPerUnit;
+    float v[EPU];
+    Elem<DT>::unpack(raw, v);
+    const float2 c2 = make_float2(c, c), e2 = make_float2(-e, -e);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < EPU; i += 2) {
+        const float2 y = ffma2(make_float2(v[i], v[i + 1]), c2, e2);
+        s = fadd2(s, make_float2(ex2(y.x), ex2(y.y)));
+    }
+    return s.x + s.y;
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 no_unit()  // a unit without elements: -inf throughout
+{
+    const uint32_t w = DT == SDV_F32 ? 0xff800000u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
+
+// The marked elements of a unit at -inf.
+template <int DT>
+__device__ __forceinline__ uint4 without(uint4 raw, uint32_t marks)
+{
+    uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (DT == SDV_F32) {
+            if (marks >> i & 1u) w[i] = 0xff800000u;
+        } else {
+            if (marks >> (2 * i) & 1u) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+            if (marks >> (2 * i + 1) & 1u) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A thread's running sum: z is relative to 2^e, e = m c rounded to fp32
+// (the rounded value is the reference itself, so it costs nothing).
+struct RunningSum {
+    float m, e, z;
+};
+
+template <int DT>
+__device__ __forceinline__ float max_of_unit(const uint4& raw)
+{
+    return Elem<DT>::unit_max(raw, -INFINITY);
+}
+
+__device__ __forceinline__ void raise(RunningSum& s, float m, float c)
+{
+    if (!(m <= s.m)) {
+        const float e = m * c;
+        s.z = s.m > -INFINITY ? s.z * ex2(s.e - e) : 0.f;
+        s.m = m;
+        s.e = e;
+    }
+}
+
+constexpr size_t kCacheBytes = 48 << 10;
+constexpr int kUnroll = 4;  // units a thread has in flight
+
+template <int DT, int NT, int MODE>
+__global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
+{
+    using E = Elem<DT>;
+    constexpr int EPU = E::kPerUnit;
     constexpr bool kStats = MODE != DISTILL_BACKWARD, kGrad = MODE != DISTILL_FORWARD;
     __shared__ DistillSmem<NT> sm;
-    extern __shared__ uint32_t bitmap[];
+    extern __shared__ uint4 dyn[];
+    uint4* const cache = dyn;  // kGrad with kStats: the row's first a.cached units
+    uint32_t* const bitmap = reinterpret_cast<uint32_t*>(dyn + a.cached);
     const int r = blockIdx.x, tid = threadIdx.x;
     const Row row = row_at<DT>(a.student, r, a.stride, a.V);
     const Row grow = kGrad ? row_at<DT>(a.grad, r, a.grad_stride, a.V) : row;
@@ -177,31 +246,42 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a)
         M = max_nan(M, s);
     }
     tm = block_max_f<NT>(tm, sm.part);  // a barrier: bitmap, bad and the record are there
+    // units whose 16 bytes all belong to the row: u0 .. u1 - 1
+    const int u0 = whole_unit<DT>(row, 0) ? 0 : 1;
+    const int u1 = row.n_units - (row.n_units > u0 && !whole_unit<DT>(row, row.n_units - 1) ? 1 : 0);
+    const uint4* const units = reinterpret_cast<const uint4*>(row.p);
     // the student's statistics: mo the largest of its other tokens, zo their
-    // sum against mo, M the row's maximum, Z its sum against M
-    float mo, zo, Z;
+    // sum against 2^eo, eo = mo c; M the row's maximum, Z its sum against 2^eM
+    float mo, zo, eo, eM, Z;
     if (kStats) {
-        float m = -INFINITY, z = 0.f;  // this thread's: its maximum so far, the sum against it
-        for (int u = tid; u < row.n_units; u += NT) {
-            float v[EPU];
-            load_elems<DT>(row, u, v);
-            const uint32_t marks = marks_of<DT>(bitmap, u);
-            float cm = -INFINITY;
+        RunningSum s = {-INFINITY, 0.f, 0.f};
+        for (int u = u0 + tid; u < u1; u += kUnroll * NT) {
+            uint4 raw[kUnroll];
 #pragma unroll
-            for (int e = 0; e < EPU; ++e) {
-                if (marks >> e & 1u) v[e] = -INFINITY;
-                cm = max_nan(cm, v[e]);
-            }
-            if (!(cm <= m)) {
-                z = m > -INFINITY ? z * ex2((m - cm) * a.c) : 0.f;
-                m = cm;
-            }
-            if (m > -INFINITY) {
+            for (int i = 0; i < kUnroll; ++i) raw[i] = u + i * NT < u1 ? units[u + i * NT] : no_unit<DT>();
+            float m = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < EPU; ++e) z += ex2((v[e] - m) * a.c);
+            for (int i = 0; i < kUnroll; ++i) {
+                const int ui = u + i * NT;
+                if (kGrad && ui < a.cached) cache[ui] = raw[i];
+                const uint32_t marks = ui < u1 ? marks_of<DT>(bitmap, ui) : 0u;
+                if (marks) raw[i] = without<DT>(raw[i], marks);
+                m = E::unit_max(raw[i], m);
+            }
+            raise(s, m, a.c);
+            if (s.m > -INFINITY) {
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) s.z += unit_sum<DT>(raw[i], a.c, s.e);
             }
         }
-        mo = block_max_f<NT>(m, sm.part);
+        // the row's first and last unit, where they are not whole
+        const int edge = tid == 0 && u0 > 0 ? 0 : tid == 1 && u1 < row.n_units ? row.n_units - 1 : -1;
+        if (edge >= 0) {
+            const uint4 raw = without<DT>(edge_unit<DT>(row, edge), marks_of<DT>(bitmap, edge));
+            raise(s, max_of_unit<DT>(raw), a.c);
+            if (s.m > -INFINITY) s.z += unit_sum<DT>(raw, a.c, s.e);
+        }
+        mo = block_max_f<NT>(s.m, sm.part);
         M = block_max_f<NT>(max_nan(M, mo), sm.part);
         // NaN, +Inf or nothing finite, or a bad token: loss and gradient are NaN
         const bool finite = M > -INFINITY && M < INFINITY;
@@ -214,10 +294,12 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a)
             }
             return;
         }
-        zo = block_sum_f<NT>(m > -INFINITY ? z * ex2((m - mo) * a.c) : 0.f, sm.part);
+        eo = mo > -INFINITY ? mo * a.c : 0.f;
+        eM = M * a.c;
+        zo = block_sum_f<NT>(s.m > -INFINITY ? s.z * ex2(s.e - eo) : 0.f, sm.part);
         float zs = 0.f;
-        for (int j = tid; j < k; j += NT) zs += sm.s[j] > -INFINITY ? ex2((sm.s[j] - M) * a.c) : 0.f;
-        Z = block_sum_f<NT>(zs, sm.part) + (mo > -INFINITY ? zo * ex2((mo - M) * a.c) : 0.f);
+        for (int j = tid; j < k; j += NT) zs += ex2(fmaf(sm.s[j], a.c, -eM));
+        Z = block_sum_f<NT>(zs, sm.part) + (mo > -INFINITY ? zo * ex2(eo - eM) : 0.f);
         if (stats && tid == 0) {
             stats[0] = mo;
             stats[1] = zo;
@@ -233,8 +315,11 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a)
             fill_row<DT, NT>(grow, NAN);
             return;
         }
+        eo = mo > -INFINITY ? mo * a.c : 0.f;
+        eM = M * a.c;
     }
     // the teacher's probabilities
+    constexpr float kLn2 = 0.693147180559945309f;
     const bool taught = !(tm == -INFINITY);  // false: the record is empty, nothing is learnt from the row
     float zt = 0.f;
     for (int j = tid; j < k; j += NT) zt += expf(sm.p[j] - tm);
@@ -245,12 +330,13 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a)
     float loss = 0.f;
     for (int j = tid; j < k; j += NT) {
         const float lp = (sm.p[j] - tm) - lzt, p = expf(lp);
-        if (kStats && !(p == 0.f)) loss += p * (lp - ((sm.s[j] - M) * a.inv_T - lz));
+        if (kStats && !(p == 0.f)) loss += p * (lp - (fmaf(sm.s[j], a.c, -eM) * kLn2 - lz));
         sm.p[j] = p;
     }
     if (kStats) {
         loss = block_sum_f<NT>(loss, sm.part);
-        if (!(pr == 0.f)) loss += pr * (lpr - ((mo - M) * a.inv_T + logf(zo) - lz));
+        const float lo = mo > -INFINITY ? (eo - eM) * kLn2 + logf(zo) : -INFINITY;
+        if (!(pr == 0.f)) loss += pr * (lpr - (lo - lz));
         if (tid == 0) a.loss[r] = taught ? weight * loss : 0.f;
     }
     if (!kGrad) return;
@@ -259,31 +345,63 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a)
         return;
     }
     const float scale = weight * (a.grad_loss ? a.grad_loss[r] : 1.f) * a.inv_T;
-    // another token: scale (q_i - p_r q_i / q_r), both against mo, so that
+    // another token: scale (q_i - p_r q_i / q_r), both against 2^eo, so that
     // neither factor is lost where the k tokens hold nearly all of the mass
-    const float fo = mo > -INFINITY ? scale * (ex2((mo - M) * a.c) / Z - pr / zo) : 0.f;
-    const float ref = mo > -INFINITY ? mo : 0.f;
+    const float fo = mo > -INFINITY ? scale * (ex2(eo - eM) / Z - pr / zo) : 0.f;
     const bool alike = grow.off == row.off;
-    for (int u = tid; u < row.n_units; u += NT) {
+    const float2 c2 = make_float2(a.c, a.c), e2 = make_float2(-eo, -eo), f2 = make_float2(fo, fo);
+    const auto put = [&](int u, const uint4& raw) {
         float v[EPU];
-        load_elems<DT>(row, u, v);
+        E::unpack(raw, v);
 #pragma unroll
-        for (int e = 0; e < EPU; ++e) v[e] = fo * ex2((v[e] - ref) * a.c);
+        for (int e = 0; e < EPU; e += 2) {
+            const float2 y = ffma2(make_float2(v[e], v[e + 1]), c2, e2);
+            const float2 g = fmul2(f2, make_float2(ex2(y.x), ex2(y.y)));
+            v[e] = g.x;
+            v[e + 1] = g.y;
+        }
         store_unit<DT>(grow, alike, row, u, v);
+    };
+    const int cached = kStats ? min(a.cached, u1) : 0;
+    for (int u = u0 + tid; u < cached; u += NT) put(u, cache[u]);  // a thread's own units
+    int u = u0 + tid;
+    if (u < cached) u += (cached - u + NT - 1) / NT * NT;
+    for (; u < u1; u += kUnroll * NT) {
+        uint4 raw[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) raw[i] = u + i * NT < u1 ? units[u + i * NT] : no_unit<DT>();
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            if (u + i * NT < u1) put(u + i * NT, raw[i]);
     }
+    if (tid == 0 && u0 > 0) put(0, edge_unit<DT>(row, 0));
+    if (tid == 1 && u1 < row.n_units) put(row.n_units - 1, edge_unit<DT>(row, row.n_units - 1));
     __syncthreads();  // the teacher's tokens are written over
     for (int j = tid; j < k; j += NT) {
         const int x = sm.index[j];
-        if (x >= 0) store_elem<DT>(grow, x, scale * (ex2((sm.s[j] - M) * a.c) / Z - sm.p[j]));
+        if (x >= 0) store_elem<DT>(grow, x, scale * (ex2(fmaf(sm.s[j], a.c, -eM)) / Z - sm.p[j]));
     }
 }
 
 template <int DT, int MODE>
-cudaError_t launch(const DistillArgs& a, cudaStream_t st)
+cudaError_t launch(DistillArgs a, cudaStream_t st)
 {
+    constexpr int NT = 512;
     // the bitmap, by element position from the row's first 16-byte boundary
-    const size_t smem = MODE == DISTILL_BACKWARD ? 0 : ((size_t)a.V + 2 * Elem<DT>::kPerUnit + 31) / 32 * 4;
-    distill_kernel<DT, 512, MODE><<<a.n_rows, 512, smem, st>>>(a);
+    const size_t bits = MODE == DISTILL_BACKWARD ? 0 : ((size_t)a.V + 2 * Elem<DT>::kPerUnit + 31) / 32 * 4;
+    a.cached = 0;
+    if (MODE == DISTILL_BOTH) {
+        const size_t units = (size_t)a.V / Elem<DT>::kPerUnit + 2;
+        const size_t room = kCacheBytes / 16;
+        a.cached = (int)(units < room ? units : room);
+    }
+    const size_t smem = (size_t)a.cached * 16 + bits;
+    auto* kernel = distill_kernel<DT, NT, MODE>;
+    if (MODE == DISTILL_BOTH) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<a.n_rows, NT, smem, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -149,6 +149,7 @@ struct DistillArgs {
     void* grad;              // [n_rows][grad_stride]; NULL: forward
     long long grad_stride;
     int* device_status;
+    int cached;              // units of a row kept in shared memory (set by the launcher)
 };
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t st);
 
