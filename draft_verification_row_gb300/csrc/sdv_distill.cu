@@ -124,30 +124,6 @@ __device__ void fill_row(const Row& g, float x)
 // backward call), the gradient from those statistics, or loss and gradient.
 enum { DISTILL_FORWARD = 0, DISTILL_BACKWARD = 1, DISTILL_BOTH = 2 };
 
-// The sum of 2^(x c - e) over one unit against the exponent e.
-template <int DT>
-__device__ __forceinline__ float unit_sum(const uint4& raw, float c, float e)
-{
-    constexpr int EPU = Elem<DT>::kPerUnit;
-    float v[EPU];
-    Elem<DT>::unpack(raw, v);
-    const float2 c2 = make_float2(c, c), e2 = make_float2(-e, -e);
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < EPU; i += 2) {
-        const float2 y = ffma2(make_float2(v[i], v[i + 1]), c2, e2);
-        s = fadd2(s, make_float2(ex2(y.x), ex2(y.y)));
-    }
-    return s.x + s.y;
-}
-
-template <int DT>
-__device__ __forceinline__ uint4 no_unit()  // a unit without elements: -inf throughout
-{
-    const uint32_t w = DT == SDV_F32 ? 0xff800000u : 0xff80ff80u;
-    return make_uint4(w, w, w, w);
-}
-
 // The marked elements of a unit at -inf.
 template <int DT>
 __device__ __forceinline__ uint4 without(uint4 raw, uint32_t marks)
@@ -165,25 +141,16 @@ __device__ __forceinline__ uint4 without(uint4 raw, uint32_t marks)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A thread's running sum: z is relative to 2^e, e = m c rounded to fp32
-// (the rounded value is the reference itself, so it costs nothing).
+// A thread's running sum z, against its largest element so far.
 struct RunningSum {
-    float m, e, z;
+    float m, z;
 };
-
-template <int DT>
-__device__ __forceinline__ float max_of_unit(const uint4& raw)
-{
-    return Elem<DT>::unit_max(raw, -INFINITY);
-}
 
 __device__ __forceinline__ void raise(RunningSum& s, float m, float c)
 {
     if (!(m <= s.m)) {
-        const float e = m * c;
-        s.z = s.m > -INFINITY ? s.z * ex2(s.e - e) : 0.f;
+        s.z = s.m > -INFINITY ? s.z * ex2((s.m - m) * c) : 0.f;
         s.m = m;
-        s.e = e;
     }
 }
 
@@ -251,10 +218,10 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
     const int u1 = row.n_units - (row.n_units > u0 && !whole_unit<DT>(row, row.n_units - 1) ? 1 : 0);
     const uint4* const units = reinterpret_cast<const uint4*>(row.p);
     // the student's statistics: mo the largest of its other tokens, zo their
-    // sum against 2^eo, eo = mo c; M the row's maximum, Z its sum against 2^eM
-    float mo, zo, eo, eM, Z;
+    // sum against mo; M the row's maximum, Z its sum against M
+    float mo, zo, Z;
     if (kStats) {
-        RunningSum s = {-INFINITY, 0.f, 0.f};
+        RunningSum s = {-INFINITY, 0.f};
         for (int u = u0 + tid; u < u1; u += kUnroll * NT) {
             uint4 raw[kUnroll];
 #pragma unroll
@@ -271,15 +238,15 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
             raise(s, m, a.c);
             if (s.m > -INFINITY) {
 #pragma unroll
-                for (int i = 0; i < kUnroll; ++i) s.z += unit_sum<DT>(raw[i], a.c, s.e);
+                for (int i = 0; i < kUnroll; ++i) s.z += unit_sum<DT>(raw[i], a.c, s.m);
             }
         }
         // the row's first and last unit, where they are not whole
         const int edge = tid == 0 && u0 > 0 ? 0 : tid == 1 && u1 < row.n_units ? row.n_units - 1 : -1;
         if (edge >= 0) {
             const uint4 raw = without<DT>(edge_unit<DT>(row, edge), marks_of<DT>(bitmap, edge));
-            raise(s, max_of_unit<DT>(raw), a.c);
-            if (s.m > -INFINITY) s.z += unit_sum<DT>(raw, a.c, s.e);
+            raise(s, E::unit_max(raw, -INFINITY), a.c);
+            if (s.m > -INFINITY) s.z += unit_sum<DT>(raw, a.c, s.m);
         }
         mo = block_max_f<NT>(s.m, sm.part);
         M = block_max_f<NT>(max_nan(M, mo), sm.part);
@@ -294,12 +261,10 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
             }
             return;
         }
-        eo = mo > -INFINITY ? mo * a.c : 0.f;
-        eM = M * a.c;
-        zo = block_sum_f<NT>(s.m > -INFINITY ? s.z * ex2(s.e - eo) : 0.f, sm.part);
+        zo = block_sum_f<NT>(s.m > -INFINITY ? s.z * ex2((s.m - mo) * a.c) : 0.f, sm.part);
         float zs = 0.f;
-        for (int j = tid; j < k; j += NT) zs += ex2(fmaf(sm.s[j], a.c, -eM));
-        Z = block_sum_f<NT>(zs, sm.part) + (mo > -INFINITY ? zo * ex2(eo - eM) : 0.f);
+        for (int j = tid; j < k; j += NT) zs += ex2((sm.s[j] - M) * a.c);
+        Z = block_sum_f<NT>(zs, sm.part) + (mo > -INFINITY ? zo * ex2((mo - M) * a.c) : 0.f);
         if (stats && tid == 0) {
             stats[0] = mo;
             stats[1] = zo;
@@ -315,11 +280,8 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
             fill_row<DT, NT>(grow, NAN);
             return;
         }
-        eo = mo > -INFINITY ? mo * a.c : 0.f;
-        eM = M * a.c;
     }
     // the teacher's probabilities
-    constexpr float kLn2 = 0.693147180559945309f;
     const bool taught = !(tm == -INFINITY);  // false: the record is empty, nothing is learnt from the row
     float zt = 0.f;
     for (int j = tid; j < k; j += NT) zt += expf(sm.p[j] - tm);
@@ -330,12 +292,12 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
     float loss = 0.f;
     for (int j = tid; j < k; j += NT) {
         const float lp = (sm.p[j] - tm) - lzt, p = expf(lp);
-        if (kStats && !(p == 0.f)) loss += p * (lp - (fmaf(sm.s[j], a.c, -eM) * kLn2 - lz));
+        if (kStats && !(p == 0.f)) loss += p * (lp - ((sm.s[j] - M) * a.inv_T - lz));
         sm.p[j] = p;
     }
     if (kStats) {
         loss = block_sum_f<NT>(loss, sm.part);
-        const float lo = mo > -INFINITY ? (eo - eM) * kLn2 + logf(zo) : -INFINITY;
+        const float lo = mo > -INFINITY ? (mo - M) * a.inv_T + logf(zo) : -INFINITY;
         if (!(pr == 0.f)) loss += pr * (lpr - (lo - lz));
         if (tid == 0) a.loss[r] = taught ? weight * loss : 0.f;
     }
@@ -345,17 +307,18 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
         return;
     }
     const float scale = weight * (a.grad_loss ? a.grad_loss[r] : 1.f) * a.inv_T;
-    // another token: scale (q_i - p_r q_i / q_r), both against 2^eo, so that
+    // another token: scale (q_i - p_r q_i / q_r), both against mo, so that
     // neither factor is lost where the k tokens hold nearly all of the mass
-    const float fo = mo > -INFINITY ? scale * (ex2(eo - eM) / Z - pr / zo) : 0.f;
+    const float fo = mo > -INFINITY ? scale * (ex2((mo - M) * a.c) / Z - pr / zo) : 0.f;
     const bool alike = grow.off == row.off;
-    const float2 c2 = make_float2(a.c, a.c), e2 = make_float2(-eo, -eo), f2 = make_float2(fo, fo);
+    const float ref = mo > -INFINITY ? mo : 0.f;
+    const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-ref, -ref), f2 = make_float2(fo, fo);
     const auto put = [&](int u, const uint4& raw) {
         float v[EPU];
         E::unpack(raw, v);
 #pragma unroll
         for (int e = 0; e < EPU; e += 2) {
-            const float2 y = ffma2(make_float2(v[e], v[e + 1]), c2, e2);
+            const float2 y = fmul2(fadd2(make_float2(v[e], v[e + 1]), m2), c2);
             const float2 g = fmul2(f2, make_float2(ex2(y.x), ex2(y.y)));
             v[e] = g.x;
             v[e + 1] = g.y;
@@ -379,7 +342,7 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
     __syncthreads();  // the teacher's tokens are written over
     for (int j = tid; j < k; j += NT) {
         const int x = sm.index[j];
-        if (x >= 0) store_elem<DT>(grow, x, scale * (ex2(fmaf(sm.s[j], a.c, -eM)) / Z - sm.p[j]));
+        if (x >= 0) store_elem<DT>(grow, x, scale * (ex2((sm.s[j] - M) * a.c) / Z - sm.p[j]));
     }
 }
 

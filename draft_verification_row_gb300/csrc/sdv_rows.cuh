@@ -76,6 +76,19 @@ __device__ __forceinline__ uint4 load_unit(const Row& row, int u)
 }
 
 template <int DT>
+__device__ __forceinline__ uint4 no_unit()  // a unit without elements: -inf throughout
+{
+    const uint32_t w = DT == SDV_F32 ? 0xff800000u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 load_unit_or_none(const Row& row, int u)
+{
+    return u >= 0 && u < row.n_units ? load_unit<DT>(row, u) : no_unit<DT>();
+}
+
+template <int DT>
 __device__ __forceinline__ void load_elems(const Row& row, int u, float (&v)[Elem<DT>::kPerUnit])
 {
     Elem<DT>::unpack(load_unit<DT>(row, u), v);
@@ -351,5 +364,311 @@ __device__ Border find_border(const Src& src, bool mass, u64 need, uint32_t klo,
     }
 }
 
+// ------------------------------------------------------------------------
+// groups: the maximum (and the mass) of every 128-byte line of a row, kept
+// in shared memory by the one pass that reads the row from HBM.  The k-th
+// largest group maximum is a lower bound of the k-th largest logit, so what
+// follows reads only the lines whose maximum reaches it: about k of 2374
+// for a row of 151936 bf16 logits.  Rows of up to kUnitGroups units keep
+// every 16-byte unit's maximum instead (their k may come near the number of
+// lines).
+
+constexpr int kUnitGroups = 8192;
+constexpr int kSegU = 256;  // units per segment: a warp's step of 8 per lane
+
+__host__ __device__ inline int units_bound(int V, int per_unit) { return (V + 2 * per_unit - 2) / per_unit; }
+
+// Groups of the longest row of V elements, at any alignment.
+__host__ __device__ inline int groups_bound(int V, int per_unit)
+{
+    const int u = units_bound(V, per_unit);
+    if ((V + per_unit - 1) / per_unit <= kUnitGroups) return u < kUnitGroups ? u : kUnitGroups;
+    return (u + kSegU - 1) / kSegU * (kSegU / 8);  // whole segments: a step writes all of its 32 lines
+}
+
+struct Groups {
+    float* max;  // [n]
+    float* sum;  // [n]: sum of 2^((x - max) c) over the group
+    int n;
+    int width;  // units per group: 1 or 8
+};
+
+template <int DT>
+__device__ __forceinline__ Groups groups_of(const Row& row, float* max, float* sum)
+{
+    Groups g;
+    g.max = max;
+    g.sum = sum;
+    g.width = row.n_units <= kUnitGroups ? 1 : 8;
+    g.n = (row.n_units + g.width - 1) / g.width;
+    return g;
+}
+
+// The sum of 2^((x - m) c) over one unit, m no less than its elements.  The
+// difference comes first: x c would overflow for the lowest finite values,
+// which masks write.
+template <int DT>
+__device__ __forceinline__ float unit_sum(const uint4& raw, float c, float m)
+{
+    constexpr int EPU = Elem<DT>::kPerUnit;
+    float v[EPU];
+    Elem<DT>::unpack(raw, v);
+    const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < EPU; i += 2) {
+        const float2 y = fmul2(fadd2(make_float2(v[i], v[i + 1]), m2), c2);
+        s = fadd2(s, make_float2(ex2(y.x), ex2(y.y)));
+    }
+    return s.x + s.y;
+}
+
+// A unit's maximum, packed as its type packs it, and the larger of two.
+template <int DT>
+__device__ __forceinline__ uint32_t packed_max(const uint4& u)
+{
+    if (DT == SDV_F32) return __float_as_uint(Elem<DT>::unit_max(u, -INFINITY));
+    return max_nan_bf16x2(max_nan_bf16x2(u.x, u.y), max_nan_bf16x2(u.z, u.w));
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
+{
+    if (DT == SDV_F32) return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    return max_nan_bf16x2(a, b);
+}
+
+template <int DT>
+__device__ __forceinline__ float unpacked_max(uint32_t a)
+{
+    if (DT == SDV_F32) return __uint_as_float(a);
+    return max_nan(bf_lo(a), bf_hi(a));
+}
+
+// Eight values per lane, value i belonging with those of the lane's
+// neighbours in its aligned eight lanes: lane j of the eight gets value j
+// reduced over them.  Seven exchanges in place of twenty-four.
+template <class T, class F>
+__device__ __forceinline__ T scatter_reduce(const T (&p)[8], int lane, F op)
+{
+    T q[4], r[2];
+    const bool b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const T other = __shfl_xor_sync(0xffffffffu, b2 ? p[i] : p[i + 4], 4);
+        q[i] = op(b2 ? p[i + 4] : p[i], other);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const T other = __shfl_xor_sync(0xffffffffu, b1 ? q[i] : q[i + 2], 2);
+        r[i] = op(b1 ? q[i + 2] : q[i], other);
+    }
+    const T other = __shfl_xor_sync(0xffffffffu, b0 ? r[0] : r[1], 1);
+    return op(b0 ? r[1] : r[0], other);
+}
+
+// Reads the row once: every group's maximum, and with SUMS its mass against
+// that maximum (c: log2(e) / T).  Returns the thread's largest value (NaN if
+// it met one).
+template <int DT, int NT, bool SUMS>
+__device__ float scan_groups(const Row& row, const Groups& g, float c)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    float best = -INFINITY;
+    if (g.width == 1) {
+        constexpr int U = 4;
+        for (int u = threadIdx.x; u < row.n_units; u += U * NT) {
+            uint4 raw[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) raw[i] = load_unit_or_none<DT>(row, u + i * NT);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (u + i * NT >= row.n_units) break;
+                const float m = Elem<DT>::unit_max(raw[i], -INFINITY);
+                best = max_nan(best, m);
+                g.max[u + i * NT] = m;
+                if (SUMS) g.sum[u + i * NT] = m > -INFINITY ? unit_sum<DT>(raw[i], c, m) : 0.f;
+            }
+        }
+        return best;
+    }
+    const int n_seg = (row.n_units + kSegU - 1) / kSegU;
+    for (int s = w; s < n_seg; s += NT / 32) {
+        const int u = s * kSegU + lane;
+        uint4 raw[8];
+        if (s > 0 && s + 1 < n_seg) {
+            const uint4* p = reinterpret_cast<const uint4*>(row.p) + u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) raw[i] = p[i * 32];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) raw[i] = load_unit_or_none<DT>(row, u + i * 32);
+        }
+        uint32_t p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = packed_max<DT>(raw[i]);
+        const float m = unpacked_max<DT>(
+            scatter_reduce(p, lane, [](uint32_t a, uint32_t b) { return larger<DT>(a, b); }));
+        best = max_nan(best, m);
+        const int line = s * 32 + (lane & 7) * 4 + (lane >> 3);
+        g.max[line] = m;
+        if (SUMS) {
+            float z[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float mi = __shfl_sync(0xffffffffu, m, (lane & 24) | i);
+                z[i] = mi > -INFINITY ? unit_sum<DT>(raw[i], c, mi) : 0.f;
+            }
+            g.sum[line] = scatter_reduce(z, lane, [](float a, float b) { return a + b; });
+        }
+    }
+    return best;
+}
+
+// Buckets by the distance from the row's maximum, 32 to an octave, whatever
+// the logits' scale: 0 is within 2^-13 of it, the last one (kFar) 2^19 or
+// more below it, -inf among them.
+constexpr int kFar = kBuckets - 1;
+
+__device__ __forceinline__ int bucket_of(float x, float M)
+{
+    const int b = (int)(__float_as_uint(M - x) >> 18) - ((127 - 13) << 5);
+    return min(max(b, 0), kFar);
+}
+
+// Calls f(raw, u) for each unit u of the groups with sel(maximum), by whole
+// warps: a warp has a contiguous range of the groups, and its lanes hold
+// their units in index order (lanes without a unit: no_unit, u = -1).
+template <int DT, int NT, class S, class F>
+__device__ void for_selected(const Row& row, const Groups& g, S sel, F f)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int per = (g.n + NT / 32 - 1) / (NT / 32);
+    const int g1 = min((w + 1) * per, g.n);
+    for (int gb = w * per; gb < g1; gb += 32) {
+        const int gi = gb + lane;
+        const bool mine = gi < g1 && sel(g.max[gi]);
+        unsigned mask = __ballot_sync(0xffffffffu, mine);
+        if (g.width == 1) {
+            if (mask) f(mine ? load_unit<DT>(row, gi) : no_unit<DT>(), mine ? gi : -1);
+            continue;
+        }
+        while (mask) {
+            unsigned m = mask;
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (j < lane >> 3) m &= m - 1;
+            const int u = m ? (gb + __ffs(m) - 1) * 8 + (lane & 7) : -1;
+            const bool there = u >= 0 && u < row.n_units;
+            f(there ? load_unit<DT>(row, u) : no_unit<DT>(), there ? u : -1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mask &= mask - 1;
+        }
+    }
+}
+
+// A listed token: its key and index.
+__device__ __forceinline__ u64 list_entry(uint32_t key, int x) { return (u64)key << 32 | (uint32_t)x; }
+__device__ __forceinline__ uint32_t entry_key(u64 e) { return (uint32_t)(e >> 32); }
+__device__ __forceinline__ int entry_index(u64 e) { return (int)(uint32_t)e; }
+
+// The finite logits in buckets 0..top of a row, listed in index order;
+// returns how many there are (more than cap: none are listed).  rest(x): is
+// called, where something is listed, for each element of the groups read
+// that is not.  All threads; ends with a barrier.
+template <int DT, int NT, class R>
+__device__ int collect(const Row& row, const Groups& g, float M, int top, u64* list, int cap, BlockSmem<NT>& bs,
+                       R rest)
+{
+    constexpr int EPU = Elem<DT>::kPerUnit;
+    const int lane = threadIdx.x & 31;
+    const auto in = [&](float x) { return x > -INFINITY && bucket_of(x, M) <= top; };
+    const auto hits = [&](const uint4& raw, float (&v)[EPU]) {
+        Elem<DT>::unpack(raw, v);
+        uint32_t h = 0;
+#pragma unroll
+        for (int e = 0; e < EPU; ++e) h |= (in(v[e]) ? 1u : 0u) << e;
+        return h;
+    };
+    int count = 0;
+    for_selected<DT, NT>(row, g, in, [&](const uint4& raw, int) {
+        float v[EPU];
+        count += __popc(hits(raw, v));
+    });
+    count = __reduce_add_sync(0xffffffffu, count);
+    // warps in order: where this warp's tokens begin
+    __syncthreads();
+    if (lane == 0) bs.part[threadIdx.x >> 5] = (u64)count;
+    __syncthreads();
+    int at = 0, n = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        if (i < (int)(threadIdx.x >> 5)) at += (int)bs.part[i];
+        n += (int)bs.part[i];
+    }
+    if (n <= cap && count > 0) {
+        for_selected<DT, NT>(row, g, in, [&](const uint4& raw, int u) {
+            float v[EPU];
+            const uint32_t h = hits(raw, v);
+            const int mine = __popc(h);
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
+            }
+            int to = at + incl - mine;
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) {
+                if (h >> e & 1)
+                    list[to++] = list_entry(key_of<DT>(v[e]), u * EPU + e - row.off);
+                else
+                    rest(v[e]);
+            }
+            at += __shfl_sync(0xffffffffu, incl, 31);
+        });
+    }
+    __syncthreads();
+    return n;
+}
+
+// The bucket by which k groups have their maximum: at least k tokens lie in
+// buckets 0 to it.  kFar if there are fewer groups nearer than that.
+template <int NT>
+__device__ int bucket_of_kth(const Groups& g, float M, int k, Hist& h, BlockSmem<NT>& bs)
+{
+    constexpr int kPer = kBuckets / NT;
+    const int tid = threadIdx.x;
+    __syncthreads();
+    for (int i = tid; i < kBuckets; i += NT) h.lo[i] = 0u;
+    if (tid == 0) bs.bucket = kFar;
+    __syncthreads();
+    for (int i = tid; i < g.n; i += NT) atomicAdd(&h.lo[bucket_of(g.max[i], M)], 1u);
+    __syncthreads();
+    uint32_t v[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += v[i] = h.lo[tid * kPer + i];
+    u64 total;
+    uint32_t run = (uint32_t)block_scan<NT>(sum, total, bs);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (run < (uint32_t)k && run + v[i] >= (uint32_t)k) bs.bucket = tid * kPer + i;
+        run += v[i];
+    }
+    __syncthreads();
+    return bs.bucket;
+}
+
+// A list's tokens, by threads, for find_border.
+template <int DT, int NT>
+struct ListSource {
+    const u64* list;
+    int n;
+    template <class F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        for (int i = threadIdx.x; i < n; i += NT) f(key_value<DT>(entry_key(list[i])));
+    }
+};
 }  // namespace
 }  // namespace sdv

@@ -3,10 +3,15 @@
 // temperature: what a draft model needs of the target's rows to be trained
 // on them.
 //
-// One CTA per row: the maximum, the border of the first k (find_border),
-// the kept tokens listed in index order and sorted, then the others' sum
-// against the largest of them, so that a tail of 1e-9 of the row's mass
-// keeps its digits.
+// One CTA per row, and one pass over it from HBM, which keeps the maximum and
+// the mass of every 128-byte line in shared memory.  The lines whose maximum
+// is among the k largest maxima hold the k largest logits: they are read
+// again (from L2), what may be among the k is listed, cut at the k-th and
+// sorted, and the others' sum is that of the lines that were not read again
+// and of what is left in those that were: a direct sum, never the row's
+// less the listed, which would lose a tail of 1e-9 of the row's mass.  Where
+// that list would be too long (k near the number of lines, ties), the border
+// is searched over the row itself.
 #include "sdv_internal.h"
 #include "sdv_rows.cuh"
 
@@ -27,6 +32,8 @@ struct TopSource {
         }
     }
 };
+
+constexpr int kTopList = 4096;  // tokens that may be among the k largest
 
 template <int NT>
 struct TopSmem {
@@ -56,17 +63,103 @@ __device__ void sort_list(u64* list, int n)
     __syncthreads();
 }
 
+// The first k tokens from the row itself, in sm.list in index order; returns
+// how many there are, and the border: tokens with a key above it and those
+// of that key up to index `last` are listed.
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT) top_kernel(TopArgs a)
+__device__ int top_of_row(const Row& row, int k, float M, TopSmem<NT>& sm, uint32_t& key)
 {
-    using E = Elem<DT>;
-    constexpr int EPU = E::kPerUnit;
+    constexpr int EPU = Elem<DT>::kPerUnit;
+    const int tid = threadIdx.x;
+    const TopSource<DT, NT> src{row};
+    Scale none = {};
+    const Border b = find_border<DT, NT>(src, false, (u64)k, lowest_finite_key<DT>(), key_of<DT>(M), none, nullptr,
+                                         sm.hist, sm.bs);
+    const int ties = b.found ? k - (int)b.above : k;  // of the border's key
+    key = b.key;
+    // listed in index order, a thread's consecutive units at a time
+    const int per = (row.n_units + NT - 1) / NT;
+    const int u0 = min(tid * per, row.n_units), u1 = min(u0 + per, row.n_units);
+    const auto amount = [&](uint32_t x) { return x > b.key ? 1ull : x == b.key ? 1ull << 32 : 0ull; };
+    u64 count = 0;  // above the border's key | of that key << 32
+    for (int u = u0; u < u1; ++u) {
+        float v[EPU];
+        load_elems<DT>(row, u, v);
+#pragma unroll
+        for (int e = 0; e < EPU; ++e) count += amount(key_of<DT>(v[e]));
+    }
+    u64 total;
+    u64 at = block_scan<NT>(count, total, sm.bs);
+    for (int u = u0; u < u1; ++u) {
+        float v[EPU];
+        load_elems<DT>(row, u, v);
+#pragma unroll
+        for (int e = 0; e < EPU; ++e) {
+            const uint32_t x = key_of<DT>(v[e]);
+            const int before = (int)(uint32_t)at, tied = (int)(at >> 32);
+            if (x > b.key || (x == b.key && tied < ties))
+                sm.list[before + min(tied, ties)] = list_entry(~x, u * EPU + e - row.off);
+            at += amount(x);
+        }
+    }
+    __syncthreads();
+    return b.found ? k : (int)b.above;
+}
+
+// The same from the lines that may hold them; -1: too many candidates.
+template <int DT, int NT>
+__device__ int top_of_lines(const Row& row, const Groups& g, int k, float M, u64* cand, int& top, TopSmem<NT>& sm,
+                            uint32_t& key)
+{
+    const int tid = threadIdx.x;
+    top = row.V <= kTopList ? kFar : bucket_of_kth<NT>(g, M, k, sm.hist, sm.bs);
+    if (top == kFar && row.V > kTopList) return -1;
+    const int c = collect<DT, NT>(row, g, M, top, cand, kTopList, sm.bs, [](float) {});
+    if (c > kTopList) return -1;
+    const ListSource<DT, NT> src{cand, c};
+    uint32_t low = ~0u;
+    for (int i = tid; i < c; i += NT) low = min(low, entry_key(cand[i]));
+    low = __reduce_min_sync(0xffffffffu, low);
+    if ((tid & 31) == 0) sm.bs.part[tid >> 5] = low;
+    __syncthreads();
+    for (int i = 0; i < NT / 32; ++i) low = min(low, (uint32_t)sm.bs.part[i]);
+    Border b;
+    b.found = false;
+    if (c > k) {
+        Scale none = {};
+        b = find_border<DT, NT>(src, false, (u64)k, low, key_of<DT>(M), none, nullptr, sm.hist, sm.bs);
+    }
+    const int ties = b.found ? k - (int)b.above : 0;
+    key = b.found ? b.key : low;
+    const auto amount = [&](u64 e) {
+        return !b.found || entry_key(e) > b.key ? 1ull : entry_key(e) == b.key ? 1ull << 32 : 0ull;
+    };
+    const int per = (c + NT - 1) / NT, i0 = min(tid * per, c), i1 = min(i0 + per, c);
+    u64 count = 0, total;
+    for (int i = i0; i < i1; ++i) count += amount(cand[i]);
+    u64 at = block_scan<NT>(count, total, sm.bs);
+    for (int i = i0; i < i1; ++i) {
+        const u64 e = cand[i], n = amount(e);
+        const int before = (int)(uint32_t)at, tied = (int)(at >> 32);
+        if (n == 1 || (n > 1 && tied < ties)) sm.list[before + min(tied, ties)] = list_entry(~entry_key(e), entry_index(e));
+        at += n;
+    }
+    __syncthreads();
+    return min(c, k);
+}
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int groups)
+{
+    constexpr int EPU = Elem<DT>::kPerUnit;
     __shared__ TopSmem<NT> sm;
+    extern __shared__ u64 cand[];  // [kTopList], then the groups' maxima and sums
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const Row row = row_at<DT>(a.logits, r, a.stride, a.V);
-    float m = -INFINITY;
-    for (int u = tid; u < row.n_units; u += NT) m = E::unit_max(load_unit<DT>(row, u), m);
-    const float M = block_max_nan<NT>(m, sm.bs);
+    float* const gmax = reinterpret_cast<float*>(cand + kTopList);
+    const Groups g = groups_of<DT>(row, gmax, gmax + groups);
+    const float c = (float)a.c;
+    const float M = block_max_nan<NT>(scan_groups<DT, NT, true>(row, g, c), sm.bs);
     const size_t o = (size_t)r * a.k;
     if (!(M > -INFINITY && M < INFINITY)) {
         for (int i = tid; i < a.k; i += NT) {
@@ -82,99 +175,90 @@ __global__ void __launch_bounds__(NT) top_kernel(TopArgs a)
         }
         return;
     }
-    const TopSource<DT, NT> src{row};
-    const uint32_t kmin = lowest_finite_key<DT>();
-    Scale none = {};
-    const Border b = find_border<DT, NT>(src, false, (u64)a.k, kmin, key_of<DT>(M), none, nullptr, sm.hist, sm.bs);
-    const int n = b.found ? a.k : (int)b.above;             // listed tokens
-    const int ties = b.found ? a.k - (int)b.above : a.k;    // of the border's key
-    // listed in index order, a thread's consecutive units at a time
-    const int per = (row.n_units + NT - 1) / NT;
-    const int u0 = min(tid * per, row.n_units), u1 = min(u0 + per, row.n_units);
-    u64 count = 0;  // above the border's key | of that key << 32
-    for (int u = u0; u < u1; ++u) {
-        float v[EPU];
-        load_elems<DT>(row, u, v);
-#pragma unroll
-        for (int e = 0; e < EPU; ++e) {
-            const uint32_t k = key_of<DT>(v[e]);
-            count += k > b.key ? 1ull : k == b.key ? 1ull << 32 : 0ull;
-        }
+    uint32_t key;
+    int top;
+    int n = top_of_lines<DT, NT>(row, g, a.k, M, cand, top, sm, key);
+    if (n < 0) {
+        n = top_of_row<DT, NT>(row, a.k, M, sm, key);
+        top = kFar;  // every line is read again for the others' sum
     }
-    u64 total;
-    u64 at = block_scan<NT>(count, total, sm.bs);
-    float next = -INFINITY;  // the largest of the others
-    for (int u = u0; u < u1; ++u) {
-        float v[EPU];
-        load_elems<DT>(row, u, v);
-#pragma unroll
-        for (int e = 0; e < EPU; ++e) {
-            const uint32_t k = key_of<DT>(v[e]);
-            const int before = (int)(uint32_t)at, tied = (int)(at >> 32);
-            if (k > b.key || (k == b.key && tied < ties))
-                sm.list[before + min(tied, ties)] = (u64)~k << 32 | (uint32_t)(u * EPU + e - row.off);
-            else
-                next = fmaxf(next, v[e]);
-            at += k > b.key ? 1ull : k == b.key ? 1ull << 32 : 0ull;
-        }
-    }
-    next = block_max_nan<NT>(next, sm.bs);
-    int n2 = 1;
-    while (n2 < n) n2 *= 2;
-    for (int i = n + tid; i < n2; i += NT) sm.list[i] = ~0ull;
-    __syncthreads();
-    // the last kept index of the border's key, in index order
+    // the last listed index of the lowest listed key
     int last = -1;
     for (int i = tid; i < n; i += NT)
-        if (~(uint32_t)(sm.list[i] >> 32) == b.key) last = max(last, (int)(uint32_t)sm.list[i]);
+        if (~entry_key(sm.list[i]) == key) last = max(last, entry_index(sm.list[i]));
     last = __reduce_max_sync(0xffffffffu, last);
-    __syncthreads();
     if (lane == 0) sm.part[w] = __int_as_float(last);
     __syncthreads();
     for (int i = 0; i < NT / 32; ++i) last = max(last, __float_as_int(sm.part[i]));
+    // the others: their largest, then their sum against it
+    const auto listed = [&](float x, int i) {
+        const uint32_t q = key_of<DT>(x);
+        return q > key || (q == key && i <= last);
+    };
+    const auto again = [&](float m) { return m > -INFINITY && bucket_of(m, M) <= top; };
+    float next = -INFINITY;
+    for (int i = tid; i < g.n; i += NT)
+        if (!again(g.max[i])) next = fmaxf(next, g.max[i]);
+    for_selected<DT, NT>(row, g, again, [&](const uint4& raw, int u) {
+        float v[EPU];
+        Elem<DT>::unpack(raw, v);
+#pragma unroll
+        for (int e = 0; e < EPU; ++e)
+            if (!listed(v[e], u * EPU + e - row.off)) next = fmaxf(next, v[e]);
+    });
+    next = block_max_nan<NT>(next, sm.bs);
+    float z = 0.f;
+    if (next > -INFINITY) {
+        for (int i = tid; i < g.n; i += NT)
+            if (!again(g.max[i]) && g.max[i] > -INFINITY) z += g.sum[i] * ex2((g.max[i] - next) * c);
+        for_selected<DT, NT>(row, g, again, [&](const uint4& raw, int u) {
+            float v[EPU];
+            Elem<DT>::unpack(raw, v);
+#pragma unroll
+            for (int e = 0; e < EPU; ++e)
+                if (!listed(v[e], u * EPU + e - row.off)) z += ex2((v[e] - next) * c);
+        });
+        z = warp_sum(z);
+        if (lane == 0) sm.part[w] = z;
+    }
+    int n2 = 1;
+    while (n2 < n) n2 *= 2;
+    for (int i = n + tid; i < n2; i += NT) sm.list[i] = ~0ull;
     sort_list<NT>(sm.list, n2);
     for (int i = tid; i < a.k; i += NT) {
-        const float x = i < n ? key_value<DT>(~(uint32_t)(sm.list[i] >> 32)) : -INFINITY;
-        a.index[o + i] = i < n ? (int)(uint32_t)sm.list[i] : -1;
+        const float x = i < n ? key_value<DT>(~entry_key(sm.list[i])) : -INFINITY;
+        a.index[o + i] = i < n ? entry_index(sm.list[i]) : -1;
         if (DT == SDV_F32)
             static_cast<float*>(a.values)[o + i] = x;
         else
             static_cast<unsigned short*>(a.values)[o + i] = (unsigned short)(__float_as_uint(x) >> 16);
     }
-    float z = 0.f;
-    if (next > -INFINITY) {
-        const float c = (float)a.c;
-        for (int u = tid; u < row.n_units; u += NT) {
-            float v[EPU];
-            load_elems<DT>(row, u, v);
-#pragma unroll
-            for (int e = 0; e < EPU; ++e) {
-                const uint32_t k = key_of<DT>(v[e]);
-                const bool listed = k > b.key || (k == b.key && u * EPU + e - row.off <= last);
-                z += listed ? 0.f : ex2((v[e] - next) * c);
-            }
-        }
-    }
-    z = warp_sum(z);
-    __syncthreads();
-    if (lane == 0) sm.part[w] = z;
-    __syncthreads();
     if (tid == 0) {
         z = 0.f;
-        for (int i = 0; i < NT / 32; ++i) z += sm.part[i];
+        if (next > -INFINITY)
+            for (int i = 0; i < NT / 32; ++i) z += sm.part[i];
         a.rest[r] = next > -INFINITY ? (float)((double)next * a.inv_T + (double)logf(z)) : -INFINITY;
     }
+}
+
+template <int DT>
+cudaError_t launch(const TopArgs& a, cudaStream_t st)
+{
+    constexpr int NT = 512;
+    const int groups = groups_bound(a.V, Elem<DT>::kPerUnit);
+    const size_t smem = kTopList * sizeof(u64) + (size_t)groups * 2 * sizeof(float);
+    auto* kernel = top_kernel<DT, NT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<a.n_rows, NT, smem, st>>>(a, groups);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_top(const TopArgs& a, cudaStream_t st)
 {
-    if (a.dtype == SDV_F32)
-        top_kernel<SDV_F32, 512><<<a.n_rows, 512, 0, st>>>(a);
-    else
-        top_kernel<SDV_BF16, 512><<<a.n_rows, 512, 0, st>>>(a);
-    return cudaGetLastError();
+    return a.dtype == SDV_F32 ? launch<SDV_F32>(a, st) : launch<SDV_BF16>(a, st);
 }
 
 }  // namespace sdv

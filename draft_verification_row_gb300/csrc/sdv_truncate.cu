@@ -11,17 +11,26 @@
 // prefix of one order, so the kept set is a border: a key, and the index of
 // the last token of that key that is kept.
 //
-// One CTA per row.  The row is read from HBM once, for its maximum; what
-// follows reads it from L2.  All masses are fixed-point integers
-// (weight_of), so every run gives the same tokens.
+// One CTA per row, and one pass over it from HBM, which keeps the maximum
+// (and, where the row's whole mass matters, the mass) of every 128-byte line
+// in shared memory.  From these follows a threshold above which all kept
+// tokens must lie; the lines that reach it are read again (from L2), their
+// tokens above it listed in index order, and everything else is done on the
+// list.  Where no short list can hold the kept set (flat rows, a large top_k,
+// no truncation), the same steps run over the row itself, from L2.
+//
+// All masses that decide something are fixed-point integers (weight_of), so
+// every run gives the same tokens.  The mass of what is not listed is an
+// fp32 sum with a known bound on its error; where the bound leaves the
+// border open, that mass is summed again in fixed point.
 #include "sdv_internal.h"
 #include "sdv_rows.cuh"
 
 namespace sdv {
 namespace {
 
-constexpr int kSegU = 256;                                       // units per segment: a warp's step of 8 per lane
 constexpr int kMaxSeg = (SDV_MAX_V / 4 + 1 + kSegU - 1) / kSegU;  // segments of the longest row
+constexpr int kListCap = 4096;                                    // listed tokens
 
 template <int NT>
 struct TruncSmem {
@@ -158,76 +167,360 @@ __device__ __forceinline__ Settings settings_of(const TruncArgs& a, int r)
     return s;
 }
 
-// The kept set of a row whose maximum is finite (all threads).
+// A border: tokens with a key above `key` are kept, and the first `ties` (in
+// index order) of those of that key.
+struct Cut {
+    uint32_t key;
+    u64 ties;
+};
+
+constexpr u64 kAllTies = ~0ull;
+
+// The first k tokens of the order.
+template <int DT, int NT, class Src>
+__device__ void cut_at_count(const Src& src, int k, uint32_t klo, uint32_t kmax, const Scale& sc, TruncSmem<NT>& sm,
+                             Cut& c)
+{
+    const Border b = find_border<DT, NT>(src, false, (u64)k, klo, kmax, sc, sm.table, sm.hist, sm.bs);
+    if (b.found) {
+        c.key = b.key;
+        c.ties = (u64)k - b.above;
+    }
+}
+
+// p of a mass, as the least integer that is not below it.
+__device__ __forceinline__ u64 share_of(float p, u64 mass)
+{
+    const u64 need = (u64)ceil((double)p * (double)mass);
+    return need > 1 ? need : 1;
+}
+
+// The border at which the tokens of c reach the share p of their own mass.
+template <int DT, int NT, class Src>
+__device__ void cut_at_share(const Src& src, float p, uint32_t kmax, const Scale& sc, TruncSmem<NT>& sm, Cut& c)
+{
+    // tokens of the k-th key enter by their number
+    const bool limited = c.ties != kAllTies;
+    u64 mass = 0;
+    src.each([&](float x) {
+        const uint32_t k = key_of<DT>(x);
+        if (k > c.key || (k == c.key && !limited)) mass += weight_of(x, sc, sm.table);
+    });
+    mass = block_sum<NT>(mass, sm.bs);
+    const u64 w_tie = limited ? weight_of(key_value<DT>(c.key), sc, sm.table) : 0;
+    const u64 need = share_of(p, mass + (limited ? c.ties * w_tie : 0));
+    if (mass >= need) {
+        const Border b = find_border<DT, NT>(src, true, need, limited ? c.key + 1 : c.key, kmax, sc, sm.table,
+                                             sm.hist, sm.bs);
+        const u64 w = weight_of(key_value<DT>(b.key), sc, sm.table);
+        c.key = b.key;
+        c.ties = (need - b.above + w - 1) / w;
+    } else if (w_tie > 0) {  // among the tokens of the k-th key
+        const u64 t = (need - mass + w_tie - 1) / w_tie;
+        if (t < c.ties) c.ties = t;
+    }
+}
+
+// The lowest logit that min_p keeps.
+__device__ __forceinline__ float min_p_logit(const Settings& st, float M)
+{
+    return __double2float_ru((double)M + (double)st.T * log((double)st.m));
+}
+
+template <int DT>
+__device__ __forceinline__ void cut_at_logit(float x, Cut& c)
+{
+    uint32_t k = key_of<DT>(x);
+    if (key_value<DT>(k) < x) ++k;  // the next bf16 value up
+    if (k > c.key) {
+        c.key = k;
+        c.ties = kAllTies;
+    }
+}
+
+// The kept set of a row whose maximum is finite, from the row itself.
 template <int DT, int NT>
 __device__ Kept find_kept(const Row& row, const Settings& st, const Scale& sc, TruncSmem<NT>& sm)
 {
     const uint32_t kmax = key_of<DT>(sc.M), kmin = lowest_finite_key<DT>();
     const RowSource<DT, NT> src{row};
-    uint32_t key = kmin;
-    u64 ties = ~0ull;  // tokens of that key that are kept
+    Cut c = {kmin, kAllTies};
     if (st.T == 0.f) {
-        key = kmax;
-        ties = 1;
+        c.key = kmax;
+        c.ties = 1;
     } else {
-        if (st.k > 0 && st.k < row.V) {
-            const Border b = find_border<DT, NT>(src, false, (u64)st.k, kmin, kmax, sc, sm.table, sm.hist, sm.bs);
-            if (b.found) {
-                key = b.key;
-                ties = (u64)st.k - b.above;
-            }
-        }
-        if (st.p < 1.f) {
-            // the mass of the first n_k tokens, and the border of its share
-            // p; tokens of the k-th key enter by their number
-            const bool limited = ties != ~0ull;
-            u64 mass = 0;
-            src.each([&](float x) {
-                const uint32_t k = key_of<DT>(x);
-                if (k > key || (k == key && !limited)) mass += weight_of(x, sc, sm.table);
-            });
-            mass = block_sum<NT>(mass, sm.bs);
-            const u64 w_tie = limited ? weight_of(key_value<DT>(key), sc, sm.table) : 0;
-            const u64 Z = mass + (limited ? ties * w_tie : 0);
-            u64 need = (u64)ceil((double)st.p * (double)Z);
-            if (need < 1) need = 1;
-            if (mass >= need) {
-                const Border b = find_border<DT, NT>(src, true, need, limited ? key + 1 : key, kmax, sc, sm.table,
-                                                     sm.hist, sm.bs);
-                const u64 w = weight_of(key_value<DT>(b.key), sc, sm.table);
-                key = b.key;
-                ties = (need - b.above + w - 1) / w;
-            } else if (w_tie > 0) {  // among the tokens of the k-th key
-                const u64 t = (need - mass + w_tie - 1) / w_tie;
-                if (t < ties) ties = t;
-            }
-        }
-        if (st.m > 0.f) {
-            const float x = __double2float_ru((double)sc.M + (double)st.T * log((double)st.m));
-            uint32_t k = key_of<DT>(x);
-            if (key_value<DT>(k) < x) ++k;  // the next bf16 value up
-            if (k > key) {
-                key = k;
-                ties = ~0ull;
-            }
-        }
+        if (st.k > 0 && st.k < row.V) cut_at_count<DT, NT>(src, st.k, kmin, kmax, sc, sm, c);
+        if (st.p < 1.f) cut_at_share<DT, NT>(src, st.p, kmax, sc, sm, c);
+        if (st.m > 0.f) cut_at_logit<DT>(min_p_logit(st, sc.M), c);
     }
     // the index of the last kept token of the border's key
-    Kept c;
-    c.key = key;
-    c.last = 0x7fffffff;
-    if (ties != ~0ull) {
-        segment_sums<DT, NT>(row, sm.seg, [&](float x, int) { return (u64)(key_of<DT>(x) == key ? 1 : 0); });
+    Kept kept;
+    kept.key = c.key;
+    kept.last = 0x7fffffff;
+    if (c.ties != kAllTies) {
+        const auto tied = [&](float x, int) { return (u64)(key_of<DT>(x) == c.key ? 1 : 0); };
+        __syncthreads();
+        segment_sums<DT, NT>(row, sm.seg, tied);
         __syncthreads();
         if (threadIdx.x < 32) {
-            const int i = crossing<DT>(row, sm.seg, ties - 1,
-                                       [&](float x, int) { return (u64)(key_of<DT>(x) == key ? 1 : 0); });
+            const int i = crossing<DT>(row, sm.seg, c.ties - 1, tied);
             if (threadIdx.x == 0) sm.last = i < 0 ? 0x7fffffff : i;
         }
         __syncthreads();
-        c.last = sm.last;
+        kept.last = sm.last;
     }
-    return c;
+    return kept;
+}
+
+// The bucket by which the groups' largest weights alone sum to need: the
+// tokens in buckets 0 to it have at least that mass.  kFar: they do not.
+template <int DT, int NT>
+__device__ int bucket_of_mass(const Groups& g, u64 need, const Scale& sc, TruncSmem<NT>& sm)
+{
+    constexpr int kPer = kBuckets / NT;
+    const int tid = threadIdx.x;
+    Hist& h = sm.hist;
+    __syncthreads();
+    for (int i = tid; i < kBuckets; i += NT) h.lo[i] = h.hi[i] = 0u;
+    if (tid == 0) sm.bs.bucket = kFar;
+    __syncthreads();
+    for (int i = tid; i < g.n; i += NT) {
+        const u64 w = weight_of(g.max[i], sc, sm.table);
+        if (w == 0) continue;
+        const int b = bucket_of(g.max[i], sc.M);
+        const uint32_t lo = (uint32_t)w, old = atomicAdd(&h.lo[b], lo);
+        const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
+        if (hi) atomicAdd(&h.hi[b], hi);
+    }
+    __syncthreads();
+    u64 v[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += v[i] = (u64)h.hi[tid * kPer + i] << 32 | h.lo[tid * kPer + i];
+    u64 total;
+    u64 run = block_scan<NT>(sum, total, sm.bs);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (run < need && run + v[i] >= need) sm.bs.bucket = tid * kPer + i;
+        run += v[i];
+    }
+    __syncthreads();
+    return sm.bs.bucket;
+}
+
+// The weight exp((x - M) / T) in fp32 (nothing of it is left below 2^-126).
+__device__ __forceinline__ float light_weight(float x, const Scale& sc)
+{
+    const float d = x - sc.M;
+    return d * sc.ch >= -130.f ? ex2(fmaf(d, sc.ch, d * sc.cl)) : 0.f;
+}
+
+constexpr float kOne = (float)(1ull << kWeightBits);
+
+// The mass of groups for which sel(maximum), from their fp32 sums.
+template <int NT, class S>
+__device__ u64 group_mass(const Groups& g, const Scale& sc, BlockSmem<NT>& bs, float extra, S sel)
+{
+    float z = extra;
+    for (int i = threadIdx.x; i < g.n; i += NT) {
+        const float m = g.max[i], d = m - sc.M;
+        if (!(d * sc.ch >= -130.f) || !sel(m)) continue;
+        z += g.sum[i] * ex2(fmaf(d, sc.ch, d * sc.cl));  // the group's sum is against its maximum
+    }
+    return block_sum<NT>((u64)(z * kOne), bs);
+}
+
+// The kept set by way of a list of the largest tokens; n: how many are
+// listed.  False where no short list is known to hold the kept set.
+template <int DT, int NT>
+__device__ bool list_kept(const Row& row, const Groups& g, const Settings& st, const Scale& sc, u64* list, bool sums,
+                          TruncSmem<NT>& sm, Kept& kept, int& n)
+{
+    const int tid = threadIdx.x;
+    const uint32_t kmax = key_of<DT>(sc.M);
+    const bool by_count = st.T > 0.f && st.k > 0 && st.k < row.V;
+    const float xm = st.T > 0.f && st.m > 0.f ? min_p_logit(st, sc.M) : -INFINITY;
+    const int bm = xm > -INFINITY ? bucket_of(xm, sc.M) : kFar;
+    // buckets 0..top hold the kept set, or all that min_p keeps
+    int top;
+    bool whole = false;  // every finite logit is listed
+    u64 mass = 0;        // of the row, where it came from fp32 sums
+    if (st.T == 0.f) {
+        top = 0;
+    } else if (row.V <= kListCap) {
+        top = kFar;
+        whole = true;
+    } else if (by_count) {
+        if (st.k > kListCap) return false;
+        top = bucket_of_kth<NT>(g, sc.M, st.k, sm.hist, sm.bs);
+        if (st.p >= 1.f) top = min(top, bm);
+    } else if (st.p < 1.f) {
+        mass = group_mass<NT>(g, sc, sm.bs, 0.f, [](float) { return true; });
+        top = min(bucket_of_mass<DT, NT>(g, share_of(st.p, mass + (mass >> 17)), sc, sm), bm);
+    } else {
+        top = bm;
+    }
+    if (top >= kFar && !whole) return false;
+    float rest = 0.f;
+    n = collect<DT, NT>(row, g, sc.M, top, list, kListCap, sm.bs, [&](float x) {
+        if (sums) rest += light_weight(x, sc);
+    });
+    if (n > kListCap) return false;
+    const ListSource<DT, NT> src{list, n};
+    Cut c = {0u, kAllTies};
+    if (st.T == 0.f) {
+        c.key = kmax;
+        c.ties = 1;
+    } else {
+        // the lowest key that can be listed
+        if (!whole) {
+            uint32_t low = kmax;
+            for (int i = tid; i < n; i += NT) low = min(low, entry_key(list[i]));
+            low = __reduce_min_sync(0xffffffffu, low);
+            __syncthreads();
+            if ((tid & 31) == 0) sm.bs.part[tid >> 5] = low;
+            __syncthreads();
+            for (int i = 0; i < NT / 32; ++i) low = min(low, (uint32_t)sm.bs.part[i]);
+            c.key = low;
+        } else {
+            c.key = lowest_finite_key<DT>();
+        }
+        if (by_count && n > st.k) cut_at_count<DT, NT>(src, st.k, c.key, kmax, sc, sm, c);
+        if (st.p < 1.f && (by_count || whole)) {
+            cut_at_share<DT, NT>(src, st.p, kmax, sc, sm, c);
+        } else if (st.p < 1.f) {
+            // the mass of what is not listed: fp32 sums, each weight within
+            // 2^-18 (ex2.approx 2^-22, an exponent of up to 46 rounded in
+            // three places, sums of up to 64 terms); most rows need no more
+            u64 listed = 0;
+            src.each([&](float x) { listed += weight_of(x, sc, sm.table); });
+            listed = block_sum<NT>(listed, sm.bs);
+            u64 other = group_mass<NT>(g, sc, sm.bs, rest, [&](float m) { return bucket_of(m, sc.M) > top; });
+            u64 error = (other >> 18) + 64 * NT;
+            for (;;) {
+                const u64 lo = share_of(st.p, listed + (other > error ? other - error : 0));
+                const u64 hi = share_of(st.p, listed + other + error);
+                if (listed >= lo) {
+                    const Border b = find_border<DT, NT>(src, true, lo, c.key, kmax, sc, sm.table, sm.hist, sm.bs);
+                    const u64 w = weight_of(key_value<DT>(b.key), sc, sm.table);
+                    const u64 ties = (lo - b.above + w - 1) / w;
+                    if (hi <= b.above + ties * w) {
+                        c.key = b.key;
+                        c.ties = ties;
+                        break;
+                    }
+                } else {  // the border lies below the list, which min_p ends or no one knows
+                    if (top < bm) return false;
+                    break;
+                }
+                // the border lies within the error: sum again, in fixed point
+                other = 0;
+                const RowSource<DT, NT> all{row};
+                all.each([&](float x) {
+                    if (bucket_of(x, sc.M) > top) other += weight_of(x, sc, sm.table);
+                });
+                other = block_sum<NT>(other, sm.bs);
+                error = 0;
+            }
+        }
+        if (xm > -INFINITY) cut_at_logit<DT>(xm, c);
+    }
+    kept.key = c.key;
+    kept.last = 0x7fffffff;
+    if (c.ties != kAllTies) {
+        // a thread's consecutive tokens at a time
+        const int per = (n + NT - 1) / NT, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+        u64 ties = 0, total;
+        for (int i = i0; i < i1; ++i) ties += entry_key(list[i]) == c.key ? 1 : 0;
+        u64 at = block_scan<NT>(ties, total, sm.bs);
+        if (tid == 0) sm.last = 0x7fffffff;
+        __syncthreads();
+        for (int i = i0; i < i1; ++i)
+            if (entry_key(list[i]) == c.key && ++at == c.ties) sm.last = entry_index(list[i]);
+        __syncthreads();
+        kept.last = sm.last;
+    }
+    return true;
+}
+
+__device__ __forceinline__ bool entry_kept(u64 e, const Kept& c)
+{
+    return entry_key(e) > c.key || (entry_key(e) == c.key && entry_index(e) <= c.last);
+}
+
+// The threshold that a draw's running sum has to exceed, of the sum S:
+// below S for any u, so that a uniform outside [0, 1) gives the first or the
+// last token.
+__device__ __forceinline__ u64 threshold(float uf, u64 S)
+{
+    const double u = (double)uf;
+    const u64 thr = u > 0.0 ? (u64)(fmin(u, 1.0) * (double)S) : 0;
+    return thr >= S ? S - 1 : thr;
+}
+
+// Draws from the kept tokens of a list, which is in index order.
+template <int DT, int NT>
+__device__ void draw_from_list(const u64* list, int n, const Kept& c, const Settings& st, const Scale& sc,
+                               const float* u, int n_samples, int* tokens, TruncSmem<NT>& sm)
+{
+    const int tid = threadIdx.x;
+    u64* const before = reinterpret_cast<u64*>(&sm.hist);  // per thread: the mass of earlier threads' tokens
+    static_assert(sizeof(Hist) >= NT * sizeof(u64), "room for every thread's sum");
+    const auto mass = [&](int i) {
+        const u64 e = list[i];
+        return !entry_kept(e, c) ? 0ull : st.T > 0.f ? weight_of(key_value<DT>(entry_key(e)), sc, sm.table) : 1ull;
+    };
+    const int per = (n + NT - 1) / NT;
+    u64 sum = 0, S;
+    for (int i = tid * per; i < min((tid + 1) * per, n); ++i) sum += mass(i);
+    const u64 at = block_scan<NT>(sum, S, sm.bs);
+    before[tid] = at;
+    __syncthreads();
+    for (int s = tid; s < n_samples; s += NT) {
+        const u64 thr = threshold(u ? u[s] : 0.f, S);
+        int t = 0;  // the last thread with before <= thr
+        for (int o = NT / 2; o > 0; o >>= 1)
+            if (before[t + o] <= thr) t += o;
+        u64 run = before[t];
+        int pick = -1;
+        for (int i = t * per; i < min((t + 1) * per, n) && pick < 0; ++i) {
+            run += mass(i);
+            if (run > thr) pick = entry_index(list[i]);
+        }
+        tokens[s] = pick;
+    }
+}
+
+// The row at -inf but for the kept tokens of a list.  out may be the row.
+template <int DT, int NT>
+__device__ void write_from_list(const Row& row, void* out, const u64* list, int n, const Kept& c)
+{
+    constexpr int EPU = Elem<DT>::kPerUnit;
+    const Row o = row_at<DT>(out, 0, 0, row.V);
+    const uint4 none = no_unit<DT>();
+    for (int u = threadIdx.x; u < o.n_units; u += NT) {
+        if (whole_unit<DT>(o, u)) {
+            reinterpret_cast<uint4*>(o.p)[u] = none;
+            continue;
+        }
+#pragma unroll
+        for (int e = 0; e < EPU; ++e) {
+            const int x = u * EPU + e - o.off;
+            if (x < 0 || x >= row.V) continue;
+            if (DT == SDV_F32)
+                static_cast<uint32_t*>(out)[x] = none.x;
+            else
+                static_cast<unsigned short*>(out)[x] = (unsigned short)none.x;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += NT) {
+        if (!entry_kept(list[i], c)) continue;
+        const uint32_t v = __float_as_uint(key_value<DT>(entry_key(list[i])));
+        if (DT == SDV_F32)
+            static_cast<uint32_t*>(out)[entry_index(list[i])] = v;
+        else
+            static_cast<unsigned short*>(out)[entry_index(list[i])] = (unsigned short)(v >> 16);
+    }
 }
 
 // The row with what is not kept at -inf (bad: as it is).  Aligned alike,
@@ -272,18 +565,25 @@ __device__ void write_row(const Row& row, void* out, const Kept& c, bool bad)
 }
 
 template <int DT, int NT>
-__global__ void __launch_bounds__(NT) truncate_kernel(TruncArgs a)
+__global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, int groups)
 {
     using E = Elem<DT>;
     __shared__ TruncSmem<NT> sm;
+    extern __shared__ u64 list[];  // [kListCap], then the groups' maxima and sums
     const int r = blockIdx.x;
     const int tid = threadIdx.x;
     for (int i = tid; i < 64; i += NT) sm.table[i] = kExp2Table[i];
     const Row row = row_at<DT>(a.logits, r, a.stride, a.V);
     const Settings st = settings_of(a, r);
-    float m = -INFINITY;
-    for (int u = tid; u < row.n_units; u += NT) m = E::unit_max(load_unit<DT>(row, u), m);
     Scale sc;
+    const double cc = st.ok && st.T > 0.f ? 1.4426950408889634 / (double)st.T : 0.0;
+    sc.ch = (float)cc;
+    sc.cl = (float)(cc - (double)sc.ch);
+    float* const gmax = reinterpret_cast<float*>(list + kListCap);
+    const Groups g = groups_of<DT>(row, gmax, gmax + groups);
+    // the row's whole mass matters where top_p is taken of it
+    const bool sums = st.T > 0.f && st.p < 1.f && !(st.k > 0 && st.k < a.V) && a.V > kListCap;
+    float m = sums ? scan_groups<DT, NT, true>(row, g, sc.ch) : scan_groups<DT, NT, false>(row, g, sc.ch);
     sc.M = block_max_nan<NT>(m, sm.bs);
     const bool finite = sc.M > -INFINITY && sc.M < INFINITY;
     int* const tokens = a.tokens ? a.tokens + (size_t)r * a.n_samples : nullptr;
@@ -297,9 +597,13 @@ __global__ void __launch_bounds__(NT) truncate_kernel(TruncArgs a)
             atomicOr(a.device_status, (finite ? 0 : SDV_REQ_NONFINITE) | (st.ok ? 0 : SDV_REQ_BAD_SETTING));
         return;
     }
-    const double cc = st.T > 0.f ? 1.4426950408889634 / (double)st.T : 0.0;
-    sc.ch = (float)cc;
-    sc.cl = (float)(cc - (double)sc.ch);
+    const float* const u = a.u ? a.u + (size_t)r * a.n_samples : nullptr;
+    int n = 0;
+    if (list_kept<DT, NT>(row, g, st, sc, list, sums, sm, c, n)) {
+        if (out) write_from_list<DT, NT>(row, out, list, n, c);
+        if (tokens) draw_from_list<DT, NT>(list, n, c, st, sc, u, a.n_samples, tokens, sm);
+        return;
+    }
     c = find_kept<DT, NT>(row, st, sc, sm);
     if (out) write_row<DT, NT>(row, out, c, false);
     if (!tokens) return;
@@ -313,12 +617,7 @@ __global__ void __launch_bounds__(NT) truncate_kernel(TruncArgs a)
     for (int i = tid & 31; i < (row.n_units + kSegU - 1) / kSegU; i += 32) S += sm.seg[i];
     S = warp_sum_u64(S);
     for (int s = tid >> 5; s < a.n_samples; s += NT / 32) {
-        // u S < S for u < 1; a uniform outside [0, 1) gives the first or
-        // the last token
-        const double u = a.u ? (double)a.u[(size_t)r * a.n_samples + s] : 0.0;
-        u64 thr = u > 0.0 ? (u64)(fmin(u, 1.0) * (double)S) : 0;
-        if (thr >= S) thr = S - 1;
-        const int i = crossing<DT>(row, sm.seg, thr, mass);
+        const int i = crossing<DT>(row, sm.seg, threshold(u ? u[s] : 0.f, S), mass);
         if ((tid & 31) == 0) tokens[s] = i;
     }
 }
@@ -326,7 +625,13 @@ __global__ void __launch_bounds__(NT) truncate_kernel(TruncArgs a)
 template <int DT>
 cudaError_t launch(const TruncArgs& a, cudaStream_t st)
 {
-    truncate_kernel<DT, 512><<<a.n_rows, 512, 0, st>>>(a);
+    constexpr int NT = 512;
+    const int groups = groups_bound(a.V, Elem<DT>::kPerUnit);
+    const size_t smem = kListCap * sizeof(u64) + (size_t)groups * 2 * sizeof(float);
+    auto* kernel = truncate_kernel<DT, NT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<a.n_rows, NT, smem, st>>>(a, groups);
     return cudaGetLastError();
 }
 

@@ -197,6 +197,11 @@ def test_extreme_rows(dtype):
     s[3] *= 0
     _check(s, values, index, rest, 1.0)
     _check(s, values, index, None, 1.0)
+    low = s.clone()  # masks of the type's lowest value, around the teacher's tokens and over whole stretches
+    low[:, 1000:] = torch.finfo(DT[dtype]).min
+    low[1, 30:] = torch.finfo(DT[dtype]).min
+    _check(low, values, index, rest, 1.0)
+    _check(low, values, index, None, 2.0)
     s[4, int(index[4, 0])] = float("-inf")  # a token the teacher wants and the student rules out
     loss = _check(s, values, index, rest, 1.0)
     assert float(loss[4]) == float("inf")
