@@ -629,6 +629,7 @@ static sdv::TruncArgs trunc_args(int n_rows, int V, long long row_stride, int dt
     a.top_k = top_k;
     a.top_p = top_p;
     a.min_p = min_p;
+    a.log_min_p = min_p > 0.f ? std::log((double)min_p) : 0.0;
     a.row_temperature = row_temperature;
     a.row_top_k = row_top_k;
     a.row_top_p = row_top_p;

@@ -124,36 +124,6 @@ __device__ void fill_row(const Row& g, float x)
 // backward call), the gradient from those statistics, or loss and gradient.
 enum { DISTILL_FORWARD = 0, DISTILL_BACKWARD = 1, DISTILL_BOTH = 2 };
 
-// The marked elements of a unit at -inf.
-template <int DT>
-__device__ __forceinline__ uint4 without(uint4 raw, uint32_t marks)
-{
-    uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (DT == SDV_F32) {
-            if (marks >> i & 1u) w[i] = 0xff800000u;
-        } else {
-            if (marks >> (2 * i) & 1u) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
-            if (marks >> (2 * i + 1) & 1u) w[i] = (w[i] & 0xffffu) | 0xff800000u;
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// A thread's running sum z, against its largest element so far.
-struct RunningSum {
-    float m, z;
-};
-
-__device__ __forceinline__ void raise(RunningSum& s, float m, float c)
-{
-    if (!(m <= s.m)) {
-        s.z = s.m > -INFINITY ? s.z * ex2((s.m - m) * c) : 0.f;
-        s.m = m;
-    }
-}
-
 constexpr size_t kCacheBytes = 48 << 10;
 constexpr int kUnroll = 4;  // units a thread has in flight
 
@@ -235,7 +205,7 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
                 if (marks) raw[i] = without<DT>(raw[i], marks);
                 m = E::unit_max(raw[i], m);
             }
-            raise(s, m, a.c);
+            s.raise(m, a.c);
             if (s.m > -INFINITY) {
 #pragma unroll
                 for (int i = 0; i < kUnroll; ++i) s.z += unit_sum<DT>(raw[i], a.c, s.m);
@@ -245,7 +215,7 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
         const int edge = tid == 0 && u0 > 0 ? 0 : tid == 1 && u1 < row.n_units ? row.n_units - 1 : -1;
         if (edge >= 0) {
             const uint4 raw = without<DT>(edge_unit<DT>(row, edge), marks_of<DT>(bitmap, edge));
-            raise(s, E::unit_max(raw, -INFINITY), a.c);
+            s.raise(E::unit_max(raw, -INFINITY), a.c);
             if (s.m > -INFINITY) s.z += unit_sum<DT>(raw, a.c, s.m);
         }
         mo = block_max_f<NT>(s.m, sm.part);

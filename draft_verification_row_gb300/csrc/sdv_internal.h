@@ -105,6 +105,7 @@ struct TruncArgs {
     float temperature;  // the settings of every row, where the row's array is NULL
     int top_k;
     float top_p, min_p;
+    double log_min_p;  // ln(min_p) where it is above 0
     const float* row_temperature;  // [n_rows] each, or NULL
     const int* row_top_k;
     const float* row_top_p;

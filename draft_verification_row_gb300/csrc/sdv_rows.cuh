@@ -207,6 +207,7 @@ struct BlockSmem {
     u64 total;
     u64 base;    // find_border: amount before the border's bucket
     int bucket;  // find_border: the border's bucket, or -1
+    uint32_t low;  // collect: the lowest listed key
 };
 
 __device__ __forceinline__ u64 warp_sum_u64(u64 v)
@@ -423,6 +424,42 @@ __device__ __forceinline__ float unit_sum(const uint4& raw, float c, float m)
     return s.x + s.y;
 }
 
+// A thread's running sum of 2^((x - m) c), against its largest element m so
+// far.
+struct RunningSum {
+    float m, z;
+    __device__ __forceinline__ void raise(float x, float c)
+    {
+        if (!(x <= m)) {
+            z = m > -INFINITY ? z * ex2((m - x) * c) : 0.f;
+            m = x;
+        }
+    }
+    __device__ __forceinline__ void add(float x, float sum, float c)  // sum: against x
+    {
+        if (!(x > -INFINITY)) return;
+        raise(x, c);
+        z += sum * ex2((x - m) * c);
+    }
+};
+
+// The marked elements of a unit at -inf.
+template <int DT>
+__device__ __forceinline__ uint4 without(uint4 raw, uint32_t marks)
+{
+    uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (DT == SDV_F32) {
+            if (marks >> i & 1u) w[i] = 0xff800000u;
+        } else {
+            if (marks >> (2 * i) & 1u) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+            if (marks >> (2 * i + 1) & 1u) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A unit's maximum, packed as its type packs it, and the larger of two.
 template <int DT>
 __device__ __forceinline__ uint32_t packed_max(const uint4& u)
@@ -536,100 +573,142 @@ __device__ __forceinline__ int bucket_of(float x, float M)
     return min(max(b, 0), kFar);
 }
 
-// Calls f(raw, u) for each unit u of the groups with sel(maximum), by whole
-// warps: a warp has a contiguous range of the groups, and its lanes hold
-// their units in index order (lanes without a unit: no_unit, u = -1).
-template <int DT, int NT, class S, class F>
-__device__ void for_selected(const Row& row, const Groups& g, S sel, F f)
-{
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int per = (g.n + NT / 32 - 1) / (NT / 32);
-    const int g1 = min((w + 1) * per, g.n);
-    for (int gb = w * per; gb < g1; gb += 32) {
-        const int gi = gb + lane;
-        const bool mine = gi < g1 && sel(g.max[gi]);
-        unsigned mask = __ballot_sync(0xffffffffu, mine);
-        if (g.width == 1) {
-            if (mask) f(mine ? load_unit<DT>(row, gi) : no_unit<DT>(), mine ? gi : -1);
-            continue;
-        }
-        while (mask) {
-            unsigned m = mask;
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                if (j < lane >> 3) m &= m - 1;
-            const int u = m ? (gb + __ffs(m) - 1) * 8 + (lane & 7) : -1;
-            const bool there = u >= 0 && u < row.n_units;
-            f(there ? load_unit<DT>(row, u) : no_unit<DT>(), there ? u : -1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mask &= mask - 1;
-        }
+// The finite logits in buckets 0..top: a comparison of bits, as bucket_of
+// orders distances by theirs.  kFar: every finite logit.
+struct Near {
+    float M;
+    uint32_t limit;
+    bool all;
+    __device__ Near(float M, int top)
+        : M(M), limit((uint32_t)(top + 1 + ((127 - 13) << 5)) << 18), all(top >= kFar)
+    {
     }
-}
+    __device__ __forceinline__ bool operator()(float x) const
+    {
+        return all ? x > -INFINITY : __float_as_uint(M - x) < limit;
+    }
+};
 
 // A listed token: its key and index.
 __device__ __forceinline__ u64 list_entry(uint32_t key, int x) { return (u64)key << 32 | (uint32_t)x; }
 __device__ __forceinline__ uint32_t entry_key(u64 e) { return (uint32_t)(e >> 32); }
 __device__ __forceinline__ int entry_index(u64 e) { return (int)(uint32_t)e; }
 
-// The finite logits in buckets 0..top of a row, listed in index order;
-// returns how many there are (more than cap: none are listed).  rest(x): is
-// called, where something is listed, for each element of the groups read
-// that is not.  All threads; ends with a barrier.
-template <int DT, int NT, class R>
-__device__ int collect(const Row& row, const Groups& g, float M, int top, u64* list, int cap, BlockSmem<NT>& bs,
-                       R rest)
+// The logits of a row that are near (all threads), listed in index order;
+// returns how many there are, more than cap (<= 2 kBuckets * 2) where they
+// were not all listed, and the lowest listed key.  other(raw, marks): is
+// called for each unit of the lines read, with the marks of its listed
+// elements.  The lines' loads are all in flight together, so this waits for
+// L2 once (per 4 NT units); sums over four units a thread go through one
+// scan, 16 bits each.  Ends with a barrier.
+template <int DT, int NT, class F>
+__device__ int collect(const Row& row, const Groups& g, const Near& near, u64* list, int cap, uint32_t& lowest,
+                       Hist& h, BlockSmem<NT>& bs, F other)
 {
-    constexpr int EPU = Elem<DT>::kPerUnit;
-    const int lane = threadIdx.x & 31;
-    const auto in = [&](float x) { return x > -INFINITY && bucket_of(x, M) <= top; };
-    const auto hits = [&](const uint4& raw, float (&v)[EPU]) {
-        Elem<DT>::unpack(raw, v);
-        uint32_t h = 0;
-#pragma unroll
-        for (int e = 0; e < EPU; ++e) h |= (in(v[e]) ? 1u : 0u) << e;
-        return h;
-    };
+    constexpr int EPU = Elem<DT>::kPerUnit, U = 4;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    uint16_t* const lines = reinterpret_cast<uint16_t*>(&h);  // the groups to read, in order
+    // a warp's contiguous range of the groups: how many, then which
+    const int per = (g.n + NT / 32 - 1) / (NT / 32);
+    const int g0 = min(w * per, g.n), g1 = min(g0 + per, g.n);
     int count = 0;
-    for_selected<DT, NT>(row, g, in, [&](const uint4& raw, int) {
-        float v[EPU];
-        count += __popc(hits(raw, v));
-    });
+    for (int i = g0 + lane; i < g1; i += 32) count += near(g.max[i]) ? 1 : 0;
     count = __reduce_add_sync(0xffffffffu, count);
-    // warps in order: where this warp's tokens begin
     __syncthreads();
-    if (lane == 0) bs.part[threadIdx.x >> 5] = (u64)count;
+    if (lane == 0) bs.part[w] = (u64)count;
+    if (tid == 0) bs.low = ~0u;
     __syncthreads();
-    int at = 0, n = 0;
+    int at = 0, n_lines = 0;
 #pragma unroll
     for (int i = 0; i < NT / 32; ++i) {
-        if (i < (int)(threadIdx.x >> 5)) at += (int)bs.part[i];
-        n += (int)bs.part[i];
+        if (i < w) at += (int)bs.part[i];
+        n_lines += (int)bs.part[i];
     }
-    if (n <= cap && count > 0) {
-        for_selected<DT, NT>(row, g, in, [&](const uint4& raw, int u) {
-            float v[EPU];
-            const uint32_t h = hits(raw, v);
-            const int mine = __popc(h);
-            int incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += x;
-            }
-            int to = at + incl - mine;
-#pragma unroll
-            for (int e = 0; e < EPU; ++e) {
-                if (h >> e & 1)
-                    list[to++] = list_entry(key_of<DT>(v[e]), u * EPU + e - row.off);
-                else
-                    rest(v[e]);
-            }
-            at += __shfl_sync(0xffffffffu, incl, 31);
-        });
+    if (n_lines > cap) return n_lines;  // each has a near logit at least
+    for (int gb = g0; gb < g1; gb += 32) {
+        const bool mine = gb + lane < g1 && near(g.max[gb + lane]);
+        const unsigned mask = __ballot_sync(0xffffffffu, mine);
+        if (mine) lines[at + __popc(mask & ((1u << lane) - 1))] = (uint16_t)(gb + lane);
+        at += __popc(mask);
     }
     __syncthreads();
+    const int n_units = n_lines * g.width;
+    int n = 0;
+    uint32_t low = ~0u;
+    for (int p0 = 0; p0 < n_units; p0 += U * NT) {
+        uint4 raw[U];
+        int unit[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int p = p0 + i * NT + tid;
+            unit[i] = p >= n_units ? -1 : g.width == 1 ? lines[p] : lines[p >> 3] * 8 + (p & 7);
+            if (unit[i] >= row.n_units) unit[i] = -1;
+            raw[i] = unit[i] >= 0 ? load_unit<DT>(row, unit[i]) : no_unit<DT>();
+        }
+        uint32_t marks = 0;
+        u64 counts = 0;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float v[EPU];
+            Elem<DT>::unpack(raw[i], v);
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) m |= (near(v[e]) ? 1u : 0u) << e;
+            other(raw[i], m);
+            marks |= m << (8 * i);
+            counts |= (u64)__popc(m) << (16 * i);
+        }
+        u64 total;
+        u64 before = block_scan<NT>(counts, total, bs);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const uint32_t m = marks >> (8 * i) & 0xffu;
+            int to = n + (int)(before >> (16 * i) & 0xffffu);
+            if (m) {
+                float v[EPU];
+                Elem<DT>::unpack(raw[i], v);
+#pragma unroll
+                for (int e = 0; e < EPU; ++e) {
+                    if (!(m >> e & 1)) continue;
+                    const uint32_t k = key_of<DT>(v[e]);
+                    low = min(low, k);
+                    if (to < cap) list[to] = list_entry(k, unit[i] * EPU + e - row.off);
+                    ++to;
+                }
+            }
+            n += (int)(total >> (16 * i) & 0xffffu);
+        }
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0 && low != ~0u) atomicMin(&bs.low, low);
+    __syncthreads();
+    lowest = bs.low;
     return n;
+}
+
+// One entry of a list of up to NT tokens, in a thread of its own: how many
+// tokens come before it in the descending order and, with MASS, their mass
+// (w: each token's weight).  weights: NT words of scratch.
+template <int NT, bool MASS>
+__device__ __forceinline__ void rank_of(const u64* list, int n, u64 mine, u64 w, u64* weights, int& rank, u64& before)
+{
+    if (MASS) {
+        __syncthreads();
+        if ((int)threadIdx.x < n) weights[threadIdx.x] = w;
+        __syncthreads();
+    }
+    rank = 0;
+    before = 0;
+    if ((int)(threadIdx.x & ~31) >= n) return;
+    // descending keys, then ascending indexes, as one ascending number
+    const u64 order = mine ^ 0xffffffff00000000ull;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        if ((list[j] ^ 0xffffffff00000000ull) < order) {
+            ++rank;
+            if (MASS) before += weights[j];
+        }
+    }
 }
 
 // The bucket by which k groups have their maximum: at least k tokens lie in

@@ -106,31 +106,19 @@ __device__ int top_of_row(const Row& row, int k, float M, TopSmem<NT>& sm, uint3
     return b.found ? k : (int)b.above;
 }
 
-// The same from the lines that may hold them; -1: too many candidates.
-template <int DT, int NT>
-__device__ int top_of_lines(const Row& row, const Groups& g, int k, float M, u64* cand, int& top, TopSmem<NT>& sm,
-                            uint32_t& key)
+// The first k of a list longer than the block, in sm.list in index order;
+// others(x): is called for each token of the list that is not among them.
+template <int DT, int NT, class F>
+__device__ void top_of_list(const u64* cand, int c, int k, uint32_t low, float M, TopSmem<NT>& sm, F others)
 {
     const int tid = threadIdx.x;
-    top = row.V <= kTopList ? kFar : bucket_of_kth<NT>(g, M, k, sm.hist, sm.bs);
-    if (top == kFar && row.V > kTopList) return -1;
-    const int c = collect<DT, NT>(row, g, M, top, cand, kTopList, sm.bs, [](float) {});
-    if (c > kTopList) return -1;
     const ListSource<DT, NT> src{cand, c};
-    uint32_t low = ~0u;
-    for (int i = tid; i < c; i += NT) low = min(low, entry_key(cand[i]));
-    low = __reduce_min_sync(0xffffffffu, low);
-    if ((tid & 31) == 0) sm.bs.part[tid >> 5] = low;
-    __syncthreads();
-    for (int i = 0; i < NT / 32; ++i) low = min(low, (uint32_t)sm.bs.part[i]);
-    Border b;
-    b.found = false;
+    Border b = {low, 0, false};
     if (c > k) {
         Scale none = {};
         b = find_border<DT, NT>(src, false, (u64)k, low, key_of<DT>(M), none, nullptr, sm.hist, sm.bs);
     }
     const int ties = b.found ? k - (int)b.above : 0;
-    key = b.found ? b.key : low;
     const auto amount = [&](u64 e) {
         return !b.found || entry_key(e) > b.key ? 1ull : entry_key(e) == b.key ? 1ull << 32 : 0ull;
     };
@@ -141,17 +129,30 @@ __device__ int top_of_lines(const Row& row, const Groups& g, int k, float M, u64
     for (int i = i0; i < i1; ++i) {
         const u64 e = cand[i], n = amount(e);
         const int before = (int)(uint32_t)at, tied = (int)(at >> 32);
-        if (n == 1 || (n > 1 && tied < ties)) sm.list[before + min(tied, ties)] = list_entry(~entry_key(e), entry_index(e));
+        if (n == 1 || (n > 1 && tied < ties))
+            sm.list[before + min(tied, ties)] = list_entry(~entry_key(e), entry_index(e));
+        else
+            others(key_value<DT>(entry_key(e)));
         at += n;
     }
     __syncthreads();
-    return min(c, k);
+}
+
+template <int DT>
+__device__ __forceinline__ void put(const TopArgs& a, size_t at, float x, int index)
+{
+    a.index[at] = index;
+    if (DT == SDV_F32)
+        static_cast<float*>(a.values)[at] = x;
+    else
+        static_cast<unsigned short*>(a.values)[at] = (unsigned short)(__float_as_uint(x) >> 16);
 }
 
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int groups)
 {
-    constexpr int EPU = Elem<DT>::kPerUnit;
+    using E = Elem<DT>;
+    constexpr int EPU = E::kPerUnit;
     __shared__ TopSmem<NT> sm;
     extern __shared__ u64 cand[];  // [kTopList], then the groups' maxima and sums
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -162,89 +163,99 @@ __global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int group
     const float M = block_max_nan<NT>(scan_groups<DT, NT, true>(row, g, c), sm.bs);
     const size_t o = (size_t)r * a.k;
     if (!(M > -INFINITY && M < INFINITY)) {
-        for (int i = tid; i < a.k; i += NT) {
-            a.index[o + i] = -1;
-            if (DT == SDV_F32)
-                static_cast<float*>(a.values)[o + i] = NAN;
-            else
-                static_cast<unsigned short*>(a.values)[o + i] = 0x7fc0;
-        }
+        for (int i = tid; i < a.k; i += NT) put<DT>(a, o + i, __uint_as_float(0x7fc00000u), -1);
         if (tid == 0) {
             a.rest[r] = NAN;
             if (a.device_status) atomicOr(a.device_status, SDV_REQ_NONFINITE);
         }
         return;
     }
-    uint32_t key;
-    int top;
-    int n = top_of_lines<DT, NT>(row, g, a.k, M, cand, top, sm, key);
-    if (n < 0) {
-        n = top_of_row<DT, NT>(row, a.k, M, sm, key);
-        top = kFar;  // every line is read again for the others' sum
-    }
-    // the last listed index of the lowest listed key
-    int last = -1;
-    for (int i = tid; i < n; i += NT)
-        if (~entry_key(sm.list[i]) == key) last = max(last, entry_index(sm.list[i]));
-    last = __reduce_max_sync(0xffffffffu, last);
-    if (lane == 0) sm.part[w] = __int_as_float(last);
-    __syncthreads();
-    for (int i = 0; i < NT / 32; ++i) last = max(last, __float_as_int(sm.part[i]));
-    // the others: their largest, then their sum against it
-    const auto listed = [&](float x, int i) {
-        const uint32_t q = key_of<DT>(x);
-        return q > key || (q == key && i <= last);
-    };
-    const auto again = [&](float m) { return m > -INFINITY && bucket_of(m, M) <= top; };
-    float next = -INFINITY;
-    for (int i = tid; i < g.n; i += NT)
-        if (!again(g.max[i])) next = fmaxf(next, g.max[i]);
-    for_selected<DT, NT>(row, g, again, [&](const uint4& raw, int u) {
-        float v[EPU];
-        Elem<DT>::unpack(raw, v);
-#pragma unroll
-        for (int e = 0; e < EPU; ++e)
-            if (!listed(v[e], u * EPU + e - row.off)) next = fmaxf(next, v[e]);
-    });
-    next = block_max_nan<NT>(next, sm.bs);
-    float z = 0.f;
-    if (next > -INFINITY) {
+    RunningSum s = {-INFINITY, 0.f};  // of the others
+    const bool whole = row.V <= kTopList;
+    const int top = whole ? kFar : bucket_of_kth<NT>(g, M, a.k, sm.hist, sm.bs);
+    int n = kTopList + 1;  // candidates, then listed tokens
+    uint32_t low = 0;
+    if (whole || top < kFar)
+        n = collect<DT, NT>(row, g, Near(M, top), cand, kTopList, low, sm.hist, sm.bs,
+                            [&](const uint4& raw, uint32_t marks) {
+                                const uint4 left = without<DT>(raw, marks);
+                                const float m = E::unit_max(left, -INFINITY);
+                                if (!(m > -INFINITY)) return;
+                                s.raise(m, c);
+                                s.z += unit_sum<DT>(left, c, s.m);
+                            });
+    if (n <= kTopList) {
         for (int i = tid; i < g.n; i += NT)
-            if (!again(g.max[i]) && g.max[i] > -INFINITY) z += g.sum[i] * ex2((g.max[i] - next) * c);
-        for_selected<DT, NT>(row, g, again, [&](const uint4& raw, int u) {
-            float v[EPU];
-            Elem<DT>::unpack(raw, v);
+            if (!whole && bucket_of(g.max[i], M) > top) s.add(g.max[i], g.sum[i], c);
+    } else {
+        s.m = -INFINITY;
+        s.z = 0.f;
+    }
+    if (n <= NT) {  // a token in each thread: its place is the number of those before it
+        int rank;
+        u64 before;
+        const u64 e = tid < n ? cand[tid] : 0;
+        rank_of<NT, false>(cand, n, e, 0, nullptr, rank, before);
+        const float x = key_value<DT>(entry_key(e));
+        if (tid < n && rank < a.k) put<DT>(a, o + rank, x, entry_index(e));
+        if (tid < n && rank >= a.k) s.add(x, 1.f, c);
+        for (int i = n + tid; i < a.k; i += NT) put<DT>(a, o + i, -INFINITY, -1);
+    } else {
+        if (n <= kTopList) {
+            top_of_list<DT, NT>(cand, n, a.k, low, M, sm, [&](float x) { s.add(x, 1.f, c); });
+            n = min(n, a.k);
+        } else {
+            uint32_t key;
+            n = top_of_row<DT, NT>(row, a.k, M, sm, key);
+            // the last listed index of the lowest listed key, then the others
+            int last = -1;
+            for (int i = tid; i < n; i += NT)
+                if (~entry_key(sm.list[i]) == key) last = max(last, entry_index(sm.list[i]));
+            last = __reduce_max_sync(0xffffffffu, last);
+            if (lane == 0) sm.part[w] = __int_as_float(last);
+            __syncthreads();
+            for (int i = 0; i < NT / 32; ++i) last = max(last, __float_as_int(sm.part[i]));
+            for (int u = tid; u < row.n_units; u += NT) {
+                const uint4 raw = load_unit<DT>(row, u);
+                float v[EPU];
+                E::unpack(raw, v);
+                uint32_t marks = 0;
 #pragma unroll
-            for (int e = 0; e < EPU; ++e)
-                if (!listed(v[e], u * EPU + e - row.off)) z += ex2((v[e] - next) * c);
-        });
-        z = warp_sum(z);
-        if (lane == 0) sm.part[w] = z;
+                for (int i = 0; i < EPU; ++i) {
+                    const uint32_t q = key_of<DT>(v[i]);
+                    marks |= (q > key || (q == key && u * EPU + i - row.off <= last) ? 1u : 0u) << i;
+                }
+                const uint4 left = without<DT>(raw, marks);
+                const float m = E::unit_max(left, -INFINITY);
+                if (!(m > -INFINITY)) continue;
+                s.raise(m, c);
+                s.z += unit_sum<DT>(left, c, s.m);
+            }
+            __syncthreads();  // sm.part
+        }
+        int n2 = 1;
+        while (n2 < n) n2 *= 2;
+        for (int i = n + tid; i < n2; i += NT) sm.list[i] = ~0ull;
+        sort_list<NT>(sm.list, n2);
+        for (int i = tid; i < a.k; i += NT)
+            put<DT>(a, o + i, i < n ? key_value<DT>(~entry_key(sm.list[i])) : -INFINITY,
+                    i < n ? entry_index(sm.list[i]) : -1);
     }
-    int n2 = 1;
-    while (n2 < n) n2 *= 2;
-    for (int i = n + tid; i < n2; i += NT) sm.list[i] = ~0ull;
-    sort_list<NT>(sm.list, n2);
-    for (int i = tid; i < a.k; i += NT) {
-        const float x = i < n ? key_value<DT>(~entry_key(sm.list[i])) : -INFINITY;
-        a.index[o + i] = i < n ? entry_index(sm.list[i]) : -1;
-        if (DT == SDV_F32)
-            static_cast<float*>(a.values)[o + i] = x;
-        else
-            static_cast<unsigned short*>(a.values)[o + i] = (unsigned short)(__float_as_uint(x) >> 16);
-    }
+    // the others' sum, against the largest of them
+    const float next = block_max_nan<NT>(s.m, sm.bs);
+    const float z = warp_sum(s.m > -INFINITY ? s.z * ex2((s.m - next) * c) : 0.f);
+    if (lane == 0) sm.part[w] = z;
+    __syncthreads();
     if (tid == 0) {
-        z = 0.f;
-        if (next > -INFINITY)
-            for (int i = 0; i < NT / 32; ++i) z += sm.part[i];
-        a.rest[r] = next > -INFINITY ? (float)((double)next * a.inv_T + (double)logf(z)) : -INFINITY;
+        float t = 0.f;
+        for (int i = 0; i < NT / 32; ++i) t += sm.part[i];
+        a.rest[r] = next > -INFINITY ? (float)((double)next * a.inv_T + (double)logf(t)) : -INFINITY;
     }
 }
 
-template <int DT>
+template <int DT, int NT>
 cudaError_t launch(const TopArgs& a, cudaStream_t st)
 {
-    constexpr int NT = 512;
     const int groups = groups_bound(a.V, Elem<DT>::kPerUnit);
     const size_t smem = kTopList * sizeof(u64) + (size_t)groups * 2 * sizeof(float);
     auto* kernel = top_kernel<DT, NT>;
@@ -258,7 +269,8 @@ cudaError_t launch(const TopArgs& a, cudaStream_t st)
 
 cudaError_t launch_top(const TopArgs& a, cudaStream_t st)
 {
-    return a.dtype == SDV_F32 ? launch<SDV_F32>(a, st) : launch<SDV_BF16>(a, st);
+    if (a.n_rows <= 304) return a.dtype == SDV_F32 ? launch<SDV_F32, 512>(a, st) : launch<SDV_BF16, 512>(a, st);
+    return a.dtype == SDV_F32 ? launch<SDV_F32, 256>(a, st) : launch<SDV_BF16, 256>(a, st);
 }
 
 }  // namespace sdv

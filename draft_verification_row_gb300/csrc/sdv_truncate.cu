@@ -30,7 +30,9 @@ namespace sdv {
 namespace {
 
 constexpr int kMaxSeg = (SDV_MAX_V / 4 + 1 + kSegU - 1) / kSegU;  // segments of the longest row
-constexpr int kListCap = 4096;                                    // listed tokens
+constexpr int kListCap = 3072;                                    // listed tokens
+
+constexpr int kShort = 128;  // lists up to this length are ranked by counting
 
 template <int NT>
 struct TruncSmem {
@@ -39,6 +41,7 @@ struct TruncSmem {
     u64 table[64];
     u64 seg[kMaxSeg];  // per segment: tied tokens, then kept mass
     int last;          // index of the last kept token of the border's key
+    float2 min_p_off;  // T ln(min_p)
 };
 
 // The elements of a row, by threads: unit tid, tid + NT, ...
@@ -167,6 +170,19 @@ __device__ __forceinline__ Settings settings_of(const TruncArgs& a, int r)
     return s;
 }
 
+// log2(e) / T in two floats: the quotient and what it leaves, without fp64
+// (every thread needs it, and a warp's fp64 instruction holds its pipe for
+// 16 cycles).
+__device__ __forceinline__ void set_scale(Scale& sc, float T)
+{
+    constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596303e-8f;
+    sc.ch = sc.cl = 0.f;
+    if (T > 0.f) {
+        sc.ch = __fdiv_rn(kLog2e, T);
+        sc.cl = __fdiv_rn(__fadd_rn(__fmaf_rn(-sc.ch, T, kLog2e), kLog2eLo), T);
+    }
+}
+
 // A border: tokens with a key above `key` are kept, and the first `ties` (in
 // index order) of those of that key.
 struct Cut {
@@ -188,10 +204,33 @@ __device__ void cut_at_count(const Src& src, int k, uint32_t klo, uint32_t kmax,
     }
 }
 
-// p of a mass, as the least integer that is not below it.
+// f times a mass for an fp32 f in [0, 1]: the integer part of the exact
+// product, and whether anything is left of it.
+__device__ __forceinline__ u64 fraction_of(float f, u64 mass, bool& left)
+{
+    const uint32_t bits = __float_as_uint(f);
+    const int ex = (int)(bits >> 23);
+    const u64 m = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
+    const int e = 150 - (ex ? ex : 1);  // f = m 2^-e, e >= 23
+    const u64 lo = mass * m, hi = __umul64hi(mass, m);
+    if (e < 64) {
+        left = (lo & ((1ull << e) - 1)) != 0;
+        return hi << (64 - e) | lo >> e;
+    }
+    if (e < 128) {
+        left = lo != 0 || (hi & ((1ull << (e - 64)) - 1)) != 0;
+        return hi >> (e - 64);
+    }
+    left = (lo | hi) != 0;
+    return 0;
+}
+
+// p of a mass, as the least integer that is not below it (at least 1).
 __device__ __forceinline__ u64 share_of(float p, u64 mass)
 {
-    const u64 need = (u64)ceil((double)p * (double)mass);
+    bool left;
+    const u64 whole = fraction_of(p, mass, left);
+    const u64 need = whole + (left ? 1 : 0);
     return need > 1 ? need : 1;
 }
 
@@ -221,10 +260,23 @@ __device__ void cut_at_share(const Src& src, float p, uint32_t kmax, const Scale
     }
 }
 
-// The lowest logit that min_p keeps.
-__device__ __forceinline__ float min_p_logit(const Settings& st, float M)
+// The lowest fp32 number that min_p may keep, M + T ln(min_p) rounded up;
+// the second term is in two floats.
+__device__ __forceinline__ float min_p_logit(float M, float2 off)
 {
-    return __double2float_ru((double)M + (double)st.T * log((double)st.m));
+    const float s = __fadd_rn(M, off.x);
+    const float bb = __fsub_rn(s, M);
+    const float left = __fadd_rn(__fadd_rn(__fsub_rn(M, __fsub_rn(s, bb)), __fsub_rn(off.x, bb)), off.y);
+    if (!(left > 0.f)) return s;
+    return s >= 0.f ? __uint_as_float(__float_as_uint(s) + 1) : -__uint_as_float(__float_as_uint(-s) - 1);
+}
+
+// T ln(min_p) in two floats (one thread: fp64).
+__device__ __forceinline__ float2 min_p_offset(float T, double log_min_p)
+{
+    const double d = (double)T * log_min_p;
+    const float hi = (float)d;
+    return make_float2(hi, (float)(d - (double)hi));
 }
 
 template <int DT>
@@ -251,7 +303,7 @@ __device__ Kept find_kept(const Row& row, const Settings& st, const Scale& sc, T
     } else {
         if (st.k > 0 && st.k < row.V) cut_at_count<DT, NT>(src, st.k, kmin, kmax, sc, sm, c);
         if (st.p < 1.f) cut_at_share<DT, NT>(src, st.p, kmax, sc, sm, c);
-        if (st.m > 0.f) cut_at_logit<DT>(min_p_logit(st, sc.M), c);
+        if (st.m > 0.f) cut_at_logit<DT>(min_p_logit(sc.M, sm.min_p_off), c);
     }
     // the index of the last kept token of the border's key
     Kept kept;
@@ -272,30 +324,42 @@ __device__ Kept find_kept(const Row& row, const Settings& st, const Scale& sc, T
     return kept;
 }
 
-// The bucket by which the groups' largest weights alone sum to need: the
-// tokens in buckets 0 to it have at least that mass.  kFar: they do not.
-template <int DT, int NT>
-__device__ int bucket_of_mass(const Groups& g, u64 need, const Scale& sc, TruncSmem<NT>& sm)
+// The weight exp((x - M) / T) in fp32 (nothing of it is left below 2^-126).
+__device__ __forceinline__ float light_weight(float x, const Scale& sc)
+{
+    const float d = x - sc.M;
+    return d * sc.ch >= -130.f ? ex2(fmaf(d, sc.ch, d * sc.cl)) : 0.f;
+}
+
+constexpr float kOne = (float)(1ull << kWeightBits);
+
+// The bucket by which the groups' largest weights alone sum to the share p
+// of the row's mass: the tokens in buckets 0 to it have at least that mass,
+// up to the rounding of the fp32 sums.  kFar: they do not.
+template <int NT>
+__device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncSmem<NT>& sm)
 {
     constexpr int kPer = kBuckets / NT;
+    constexpr float kStep = 262144.f;  // 8192 groups of weight 1 stay below 2^31
     const int tid = threadIdx.x;
     Hist& h = sm.hist;
     __syncthreads();
-    for (int i = tid; i < kBuckets; i += NT) h.lo[i] = h.hi[i] = 0u;
+    for (int i = tid; i < kBuckets; i += NT) h.lo[i] = 0u;
     if (tid == 0) sm.bs.bucket = kFar;
     __syncthreads();
+    float z = 0.f;
     for (int i = tid; i < g.n; i += NT) {
-        const u64 w = weight_of(g.max[i], sc, sm.table);
-        if (w == 0) continue;
-        const int b = bucket_of(g.max[i], sc.M);
-        const uint32_t lo = (uint32_t)w, old = atomicAdd(&h.lo[b], lo);
-        const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
-        if (hi) atomicAdd(&h.hi[b], hi);
+        const float w = light_weight(g.max[i], sc);
+        if (w == 0.f) continue;
+        z += g.sum[i] * w;
+        const uint32_t v = (uint32_t)(w * kStep);
+        if (v) atomicAdd(&h.lo[bucket_of(g.max[i], sc.M)], v);
     }
-    __syncthreads();
+    const u64 mass = block_sum<NT>((u64)(z * kOne), sm.bs);  // finer: every thread's share is cut off
+    const u64 need = (u64)((float)mass * (p * 1.0001f) * (kStep / kOne)) + 1;
     u64 v[kPer], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += v[i] = (u64)h.hi[tid * kPer + i] << 32 | h.lo[tid * kPer + i];
+    for (int i = 0; i < kPer; ++i) sum += v[i] = h.lo[tid * kPer + i];
     u64 total;
     u64 run = block_scan<NT>(sum, total, sm.bs);
 #pragma unroll
@@ -307,118 +371,121 @@ __device__ int bucket_of_mass(const Groups& g, u64 need, const Scale& sc, TruncS
     return sm.bs.bucket;
 }
 
-// The weight exp((x - M) / T) in fp32 (nothing of it is left below 2^-126).
-__device__ __forceinline__ float light_weight(float x, const Scale& sc)
-{
-    const float d = x - sc.M;
-    return d * sc.ch >= -130.f ? ex2(fmaf(d, sc.ch, d * sc.cl)) : 0.f;
-}
-
-constexpr float kOne = (float)(1ull << kWeightBits);
-
-// The mass of groups for which sel(maximum), from their fp32 sums.
-template <int NT, class S>
-__device__ u64 group_mass(const Groups& g, const Scale& sc, BlockSmem<NT>& bs, float extra, S sel)
-{
-    float z = extra;
-    for (int i = threadIdx.x; i < g.n; i += NT) {
-        const float m = g.max[i], d = m - sc.M;
-        if (!(d * sc.ch >= -130.f) || !sel(m)) continue;
-        z += g.sum[i] * ex2(fmaf(d, sc.ch, d * sc.cl));  // the group's sum is against its maximum
-    }
-    return block_sum<NT>((u64)(z * kOne), bs);
-}
-
-// The kept set by way of a list of the largest tokens; n: how many are
-// listed.  False where no short list is known to hold the kept set.
-template <int DT, int NT>
-__device__ bool list_kept(const Row& row, const Groups& g, const Settings& st, const Scale& sc, u64* list, bool sums,
-                          TruncSmem<NT>& sm, Kept& kept, int& n)
-{
-    const int tid = threadIdx.x;
-    const uint32_t kmax = key_of<DT>(sc.M);
-    const bool by_count = st.T > 0.f && st.k > 0 && st.k < row.V;
-    const float xm = st.T > 0.f && st.m > 0.f ? min_p_logit(st, sc.M) : -INFINITY;
-    const int bm = xm > -INFINITY ? bucket_of(xm, sc.M) : kFar;
-    // buckets 0..top hold the kept set, or all that min_p keeps
+// The list that a row's kept set is taken from.
+struct List {
+    u64* at;       // in index order
+    int n;
+    uint32_t low;  // its lowest key
+    bool whole;    // every finite logit is listed
+    bool ends;     // false: buckets 0..top hold the kept set by themselves.  true: all that min_p keeps is listed
+    float rest;    // this thread's part of the fp32 mass of the lines read that is not listed
     int top;
-    bool whole = false;  // every finite logit is listed
-    u64 mass = 0;        // of the row, where it came from fp32 sums
+};
+
+// Lists what the kept set is taken from.  False where no short list is known
+// to hold it.
+template <int DT, int NT>
+__device__ bool make_list(const Row& row, const Groups& g, const Settings& st, const Scale& sc, bool sums, float xm,
+                          List& l, TruncSmem<NT>& sm)
+{
+    const int bm = xm > -INFINITY ? bucket_of(xm, sc.M) : kFar;
+    l.whole = row.V <= kListCap;
     if (st.T == 0.f) {
-        top = 0;
-    } else if (row.V <= kListCap) {
-        top = kFar;
-        whole = true;
-    } else if (by_count) {
+        l.top = 0;
+    } else if (l.whole) {
+        l.top = kFar;
+    } else if (st.k > 0 && st.k < row.V) {
         if (st.k > kListCap) return false;
-        top = bucket_of_kth<NT>(g, sc.M, st.k, sm.hist, sm.bs);
-        if (st.p >= 1.f) top = min(top, bm);
+        l.top = bucket_of_kth<NT>(g, sc.M, st.k, sm.hist, sm.bs);
+        if (st.p >= 1.f) l.top = min(l.top, bm);
     } else if (st.p < 1.f) {
-        mass = group_mass<NT>(g, sc, sm.bs, 0.f, [](float) { return true; });
-        top = min(bucket_of_mass<DT, NT>(g, share_of(st.p, mass + (mass >> 17)), sc, sm), bm);
+        l.top = min(bucket_of_share<NT>(g, st.p, sc, sm), bm);
     } else {
-        top = bm;
+        l.top = bm;
     }
-    if (top >= kFar && !whole) return false;
+    l.ends = l.top == bm;
+    if (l.top >= kFar && !l.whole) return false;
     float rest = 0.f;
-    n = collect<DT, NT>(row, g, sc.M, top, list, kListCap, sm.bs, [&](float x) {
-        if (sums) rest += light_weight(x, sc);
+    l.n = collect<DT, NT>(row, g, Near(sc.M, l.top), l.at, kListCap, l.low, sm.hist, sm.bs,
+                          [&](const uint4& raw, uint32_t marks) {
+                              if (!sums) return;
+                              float v[Elem<DT>::kPerUnit];
+                              Elem<DT>::unpack(raw, v);
+#pragma unroll
+                              for (int e = 0; e < Elem<DT>::kPerUnit; ++e)
+                                  if (!(marks >> e & 1)) rest += light_weight(v[e], sc);
+                          });
+    l.rest = rest;
+    return l.n <= kListCap;
+}
+
+// The mass of what is not listed, in fp32 sums, each weight within 2^-18
+// (ex2.approx 2^-22, an exponent of up to 46 rounded in three places, sums
+// of up to 64 terms), and the bound on its error; or, where that leaves a
+// border open, in fixed point from the row.
+template <int NT>
+__device__ u64 light_rest(const Groups& g, const List& l, const Scale& sc, u64& error, BlockSmem<NT>& bs)
+{
+    float rest = l.rest;
+    for (int i = threadIdx.x; i < g.n; i += NT)
+        if (bucket_of(g.max[i], sc.M) > l.top) rest += g.sum[i] * light_weight(g.max[i], sc);
+    const u64 other = block_sum<NT>((u64)(rest * kOne), bs);
+    error = (other >> 18) + 64 * NT;
+    return other;
+}
+
+template <int DT, int NT>
+__device__ u64 exact_rest(const Row& row, const List& l, const Scale& sc, const u64* table, BlockSmem<NT>& bs)
+{
+    u64 other = 0;
+    const RowSource<DT, NT> all{row};
+    const Near near(sc.M, l.top);
+    all.each([&](float x) {
+        if (!near(x)) other += weight_of(x, sc, table);
     });
-    if (n > kListCap) return false;
+    return block_sum<NT>(other, bs);
+}
+
+// The kept set from a longer list.  False: it is not within
+// the list.
+template <int DT, int NT>
+__device__ bool list_kept(const Row& row, const Groups& g, const Settings& st, const Scale& sc, float xm,
+                          const List& l, TruncSmem<NT>& sm, Kept& kept)
+{
+    const int tid = threadIdx.x, n = l.n;
+    const u64* const list = l.at;
+    const uint32_t kmax = key_of<DT>(sc.M);
     const ListSource<DT, NT> src{list, n};
-    Cut c = {0u, kAllTies};
+    const bool by_count = st.k > 0 && st.k < row.V;
+    Cut c = {l.low, kAllTies};
     if (st.T == 0.f) {
         c.key = kmax;
         c.ties = 1;
     } else {
-        // the lowest key that can be listed
-        if (!whole) {
-            uint32_t low = kmax;
-            for (int i = tid; i < n; i += NT) low = min(low, entry_key(list[i]));
-            low = __reduce_min_sync(0xffffffffu, low);
-            __syncthreads();
-            if ((tid & 31) == 0) sm.bs.part[tid >> 5] = low;
-            __syncthreads();
-            for (int i = 0; i < NT / 32; ++i) low = min(low, (uint32_t)sm.bs.part[i]);
-            c.key = low;
-        } else {
-            c.key = lowest_finite_key<DT>();
-        }
         if (by_count && n > st.k) cut_at_count<DT, NT>(src, st.k, c.key, kmax, sc, sm, c);
-        if (st.p < 1.f && (by_count || whole)) {
+        if (st.p < 1.f && (by_count || l.whole)) {
             cut_at_share<DT, NT>(src, st.p, kmax, sc, sm, c);
         } else if (st.p < 1.f) {
-            // the mass of what is not listed: fp32 sums, each weight within
-            // 2^-18 (ex2.approx 2^-22, an exponent of up to 46 rounded in
-            // three places, sums of up to 64 terms); most rows need no more
-            u64 listed = 0;
+            u64 listed = 0, error;
             src.each([&](float x) { listed += weight_of(x, sc, sm.table); });
             listed = block_sum<NT>(listed, sm.bs);
-            u64 other = group_mass<NT>(g, sc, sm.bs, rest, [&](float m) { return bucket_of(m, sc.M) > top; });
-            u64 error = (other >> 18) + 64 * NT;
+            u64 other = light_rest<NT>(g, l, sc, error, sm.bs);
             for (;;) {
                 const u64 lo = share_of(st.p, listed + (other > error ? other - error : 0));
                 const u64 hi = share_of(st.p, listed + other + error);
-                if (listed >= lo) {
-                    const Border b = find_border<DT, NT>(src, true, lo, c.key, kmax, sc, sm.table, sm.hist, sm.bs);
-                    const u64 w = weight_of(key_value<DT>(b.key), sc, sm.table);
-                    const u64 ties = (lo - b.above + w - 1) / w;
-                    if (hi <= b.above + ties * w) {
-                        c.key = b.key;
-                        c.ties = ties;
-                        break;
-                    }
-                } else {  // the border lies below the list, which min_p ends or no one knows
-                    if (top < bm) return false;
+                if (listed < lo) {  // the border lies below the list, which min_p ends or no one knows
+                    if (!l.ends) return false;
                     break;
                 }
-                // the border lies within the error: sum again, in fixed point
-                other = 0;
-                const RowSource<DT, NT> all{row};
-                all.each([&](float x) {
-                    if (bucket_of(x, sc.M) > top) other += weight_of(x, sc, sm.table);
-                });
-                other = block_sum<NT>(other, sm.bs);
+                const Border b = find_border<DT, NT>(src, true, lo, c.key, kmax, sc, sm.table, sm.hist, sm.bs);
+                const u64 w = weight_of(key_value<DT>(b.key), sc, sm.table);
+                const u64 ties = (lo - b.above + w - 1) / w;
+                if (hi <= b.above + ties * w) {
+                    c.key = b.key;
+                    c.ties = ties;
+                    break;
+                }
+                other = exact_rest<DT, NT>(row, l, sc, sm.table, sm.bs);
                 error = 0;
             }
         }
@@ -442,6 +509,48 @@ __device__ bool list_kept(const Row& row, const Groups& g, const Settings& st, c
     return true;
 }
 
+// The kept set of a short list, one token in each thread: the tokens
+// before each one and their mass are counted directly, and a token is kept
+// if they number less than top_k and weigh less than the share top_p.
+// Returns 1 where this thread's token is kept (w: its weight), 0 where not,
+// -1 (in all threads) where the kept set is not within the list.
+template <int DT, int NT>
+__device__ int short_kept(const Row& row, const Groups& g, const Settings& st, const Scale& sc, float xm,
+                          const List& l, u64& w, TruncSmem<NT>& sm)
+{
+    const bool mine = (int)threadIdx.x < l.n;
+    const u64 e = mine ? l.at[threadIdx.x] : 0;
+    const float x = key_value<DT>(entry_key(e));
+    const bool by_count = st.k > 0 && st.k < row.V;
+    w = !mine ? 0 : st.T > 0.f ? weight_of(x, sc, sm.table) : 1;
+    int rank;
+    u64 before;
+    rank_of<NT, true>(l.at, l.n, e, w, reinterpret_cast<u64*>(&sm.hist), rank, before);
+    if (st.T == 0.f) return mine && rank == 0;
+    bool kept = mine && (!by_count || rank < st.k);
+    if (st.p < 1.f) {
+        const u64 listed = block_sum<NT>(kept ? w : 0, sm.bs);
+        u64 other = 0, error = 0;
+        if (!by_count && !l.whole) other = light_rest<NT>(g, l, sc, error, sm.bs);
+        for (;;) {
+            const u64 lo = share_of(st.p, listed + (other > error ? other - error : 0));
+            if (listed < lo) {  // the border lies below the list, which min_p ends or no one knows
+                if (!l.ends) return -1;
+                break;
+            }
+            const u64 hi = share_of(st.p, listed + other + error);
+            const bool in = kept && before < lo;
+            if (error == 0 || !__syncthreads_or(hi > listed || (kept && before < hi) != in)) {
+                kept = in;
+                break;
+            }
+            other = exact_rest<DT, NT>(row, l, sc, sm.table, sm.bs);
+            error = 0;
+        }
+    }
+    return kept && x >= xm;
+}
+
 __device__ __forceinline__ bool entry_kept(u64 e, const Kept& c)
 {
     return entry_key(e) > c.key || (entry_key(e) == c.key && entry_index(e) <= c.last);
@@ -450,34 +559,25 @@ __device__ __forceinline__ bool entry_kept(u64 e, const Kept& c)
 // The threshold that a draw's running sum has to exceed, of the sum S:
 // below S for any u, so that a uniform outside [0, 1) gives the first or the
 // last token.
-__device__ __forceinline__ u64 threshold(float uf, u64 S)
+__device__ __forceinline__ u64 threshold(float u, u64 S)
 {
-    const double u = (double)uf;
-    const u64 thr = u > 0.0 ? (u64)(fmin(u, 1.0) * (double)S) : 0;
-    return thr >= S ? S - 1 : thr;
+    if (!(u > 0.f)) return 0;
+    if (u >= 1.f) return S - 1;
+    bool left;
+    return fraction_of(u, S, left);
 }
 
-// Draws from the kept tokens of a list, which is in index order.
-template <int DT, int NT>
-__device__ void draw_from_list(const u64* list, int n, const Kept& c, const Settings& st, const Scale& sc,
-                               const float* u, int n_samples, int* tokens, TruncSmem<NT>& sm)
+// The draws of a row whose running sums per thread are known: before[t] is
+// the kept mass of the threads before t, each of which holds the list's next
+// `per` tokens; mass(i) is the kept mass of token i.
+template <int NT, class F>
+__device__ __forceinline__ void draw_all(const u64* list, int n, int per, const u64* before, u64 S, const float* u,
+                                         int n_samples, int* tokens, F mass)
 {
-    const int tid = threadIdx.x;
-    u64* const before = reinterpret_cast<u64*>(&sm.hist);  // per thread: the mass of earlier threads' tokens
-    static_assert(sizeof(Hist) >= NT * sizeof(u64), "room for every thread's sum");
-    const auto mass = [&](int i) {
-        const u64 e = list[i];
-        return !entry_kept(e, c) ? 0ull : st.T > 0.f ? weight_of(key_value<DT>(entry_key(e)), sc, sm.table) : 1ull;
-    };
-    const int per = (n + NT - 1) / NT;
-    u64 sum = 0, S;
-    for (int i = tid * per; i < min((tid + 1) * per, n); ++i) sum += mass(i);
-    const u64 at = block_scan<NT>(sum, S, sm.bs);
-    before[tid] = at;
-    __syncthreads();
-    for (int s = tid; s < n_samples; s += NT) {
+    for (int s = threadIdx.x; s < n_samples; s += NT) {
         const u64 thr = threshold(u ? u[s] : 0.f, S);
         int t = 0;  // the last thread with before <= thr
+#pragma unroll
         for (int o = NT / 2; o > 0; o >>= 1)
             if (before[t + o] <= thr) t += o;
         u64 run = before[t];
@@ -490,9 +590,29 @@ __device__ void draw_from_list(const u64* list, int n, const Kept& c, const Sett
     }
 }
 
-// The row at -inf but for the kept tokens of a list.  out may be the row.
+// Draws from the kept tokens of a list, which is in index order.
 template <int DT, int NT>
-__device__ void write_from_list(const Row& row, void* out, const u64* list, int n, const Kept& c)
+__device__ void draw_from_list(const u64* list, int n, const Kept& c, const Settings& st, const Scale& sc,
+                               const float* u, int n_samples, int* tokens, TruncSmem<NT>& sm)
+{
+    const int tid = threadIdx.x;
+    u64* const before = reinterpret_cast<u64*>(&sm.hist);
+    static_assert(sizeof(Hist) >= NT * sizeof(u64), "room for every thread's sum");
+    const auto mass = [&](int i) {
+        const u64 e = list[i];
+        return !entry_kept(e, c) ? 0ull : st.T > 0.f ? weight_of(key_value<DT>(entry_key(e)), sc, sm.table) : 1ull;
+    };
+    const int per = (n + NT - 1) / NT;
+    u64 sum = 0, S;
+    for (int i = tid * per; i < min((tid + 1) * per, n); ++i) sum += mass(i);
+    before[tid] = block_scan<NT>(sum, S, sm.bs);
+    __syncthreads();
+    draw_all<NT>(list, n, per, before, S, u, n_samples, tokens, mass);
+}
+
+// The whole row at -inf.  out may be the row.
+template <int DT, int NT>
+__device__ void write_none(const Row& row, void* out)
 {
     constexpr int EPU = Elem<DT>::kPerUnit;
     const Row o = row_at<DT>(out, 0, 0, row.V);
@@ -512,15 +632,16 @@ __device__ void write_from_list(const Row& row, void* out, const u64* list, int 
                 static_cast<unsigned short*>(out)[x] = (unsigned short)none.x;
         }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += NT) {
-        if (!entry_kept(list[i], c)) continue;
-        const uint32_t v = __float_as_uint(key_value<DT>(entry_key(list[i])));
-        if (DT == SDV_F32)
-            static_cast<uint32_t*>(out)[entry_index(list[i])] = v;
-        else
-            static_cast<unsigned short*>(out)[entry_index(list[i])] = (unsigned short)(v >> 16);
-    }
+}
+
+template <int DT>
+__device__ __forceinline__ void write_entry(void* out, u64 e)
+{
+    const uint32_t v = __float_as_uint(key_value<DT>(entry_key(e)));
+    if (DT == SDV_F32)
+        static_cast<uint32_t*>(out)[entry_index(e)] = v;
+    else
+        static_cast<unsigned short*>(out)[entry_index(e)] = (unsigned short)(v >> 16);
 }
 
 // The row with what is not kept at -inf (bad: as it is).  Aligned alike,
@@ -576,9 +697,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
     const Row row = row_at<DT>(a.logits, r, a.stride, a.V);
     const Settings st = settings_of(a, r);
     Scale sc;
-    const double cc = st.ok && st.T > 0.f ? 1.4426950408889634 / (double)st.T : 0.0;
-    sc.ch = (float)cc;
-    sc.cl = (float)(cc - (double)sc.ch);
+    set_scale(sc, st.ok ? st.T : 0.f);
+    if (tid == 0 && st.ok && st.m > 0.f)
+        sm.min_p_off = min_p_offset(st.T, a.row_min_p ? log((double)st.m) : a.log_min_p);
     float* const gmax = reinterpret_cast<float*>(list + kListCap);
     const Groups g = groups_of<DT>(row, gmax, gmax + groups);
     // the row's whole mass matters where top_p is taken of it
@@ -598,11 +719,42 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
         return;
     }
     const float* const u = a.u ? a.u + (size_t)r * a.n_samples : nullptr;
-    int n = 0;
-    if (list_kept<DT, NT>(row, g, st, sc, list, sums, sm, c, n)) {
-        if (out) write_from_list<DT, NT>(row, out, list, n, c);
-        if (tokens) draw_from_list<DT, NT>(list, n, c, st, sc, u, a.n_samples, tokens, sm);
-        return;
+    const float xm = st.T > 0.f && st.m > 0.f ? min_p_logit(sc.M, sm.min_p_off) : -INFINITY;
+    List l;
+    l.at = list;
+    if (make_list<DT, NT>(row, g, st, sc, sums, xm, l, sm)) {
+        if (l.n <= kShort) {
+            u64 w;
+            const int kept = short_kept<DT, NT>(row, g, st, sc, xm, l, w, sm);
+            if (kept >= 0) {
+                if (out) {
+                    write_none<DT, NT>(row, out);
+                    __syncthreads();
+                    if (kept) write_entry<DT>(out, list[tid]);
+                }
+                if (tokens) {
+                    u64* const before = reinterpret_cast<u64*>(&sm.hist);
+                    u64 S;
+                    const u64 at = block_scan<NT>(kept ? w : 0, S, sm.bs);
+                    __syncthreads();
+                    before[tid] = at;
+                    __syncthreads();
+                    // a single token: the first one past the threshold is its thread's
+                    draw_all<NT>(list, l.n, 1, before, S, u, a.n_samples, tokens,
+                                 [](int) { return (u64)1 << 63; });
+                }
+                return;
+            }
+        } else if (list_kept<DT, NT>(row, g, st, sc, xm, l, sm, c)) {
+            if (out) {
+                write_none<DT, NT>(row, out);
+                __syncthreads();
+                for (int i = tid; i < l.n; i += NT)
+                    if (entry_kept(list[i], c)) write_entry<DT>(out, list[i]);
+            }
+            if (tokens) draw_from_list<DT, NT>(list, l.n, c, st, sc, u, a.n_samples, tokens, sm);
+            return;
+        }
     }
     c = find_kept<DT, NT>(row, st, sc, sm);
     if (out) write_row<DT, NT>(row, out, c, false);
@@ -622,10 +774,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
     }
 }
 
-template <int DT>
+template <int DT, int NT>
 cudaError_t launch(const TruncArgs& a, cudaStream_t st)
 {
-    constexpr int NT = 512;
     const int groups = groups_bound(a.V, Elem<DT>::kPerUnit);
     const size_t smem = kListCap * sizeof(u64) + (size_t)groups * 2 * sizeof(float);
     auto* kernel = truncate_kernel<DT, NT>;
@@ -639,7 +790,8 @@ cudaError_t launch(const TruncArgs& a, cudaStream_t st)
 
 cudaError_t launch_truncate(const TruncArgs& a, cudaStream_t st)
 {
-    return a.dtype == SDV_F32 ? launch<SDV_F32>(a, st) : launch<SDV_BF16>(a, st);
+    if (a.n_rows <= 304) return a.dtype == SDV_F32 ? launch<SDV_F32, 512>(a, st) : launch<SDV_BF16, 512>(a, st);
+    return a.dtype == SDV_F32 ? launch<SDV_F32, 256>(a, st) : launch<SDV_BF16, 256>(a, st);
 }
 
 }  // namespace sdv
