@@ -318,8 +318,13 @@ def _c_int(name, x):
     return int(x)
 
 
+_NO_ARRAYS = (None,) * 4
+
+
 def _settings(n, device, temperature, top_k, top_p, min_p):
     """The common settings and the rows' arrays of a truncated distribution: each is a number or an [n_rows] tensor."""
+    if type(temperature) is type(top_p) is type(min_p) is float and type(top_k) is int:  # the usual call, quickly
+        return (temperature, _c_int("top_k", top_k), top_p, min_p), _NO_ARRAYS
     common, arrays = [], []
     for name, x, cast, dtype in (("temperature", temperature, float, torch.float32), ("top_k", top_k, int, torch.int32),
                                  ("top_p", top_p, float, torch.float32), ("min_p", min_p, float, torch.float32)):
@@ -338,8 +343,12 @@ def _status(device_status, device):
     return _vector("device_status", device_status, 1, torch.int32, device)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _stream(stream, device):
-    return ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def sample_truncated(logits, n_samples, u, temperature, *, top_k=0, top_p=1.0, min_p=0.0, V=None, tokens=None,
@@ -366,8 +375,8 @@ def sample_truncated(logits, n_samples, u, temperature, *, top_k=0, top_p=1.0, m
           or tuple(tokens.shape) != (n, n_samples)):
         raise ValueError("tokens must be a contiguous CUDA int32 [n_rows][n_samples] tensor")
     device_status = _status(device_status, logits.device)
-    rc = h.sdv_sample_truncated(n, V, stride, _dtype_code(logits), *common, *map(_ptr, arrays), _ptr(logits), n_samples,
-                                _ptr(u), _ptr(tokens), _ptr(device_status), _stream(stream, logits.device))
+    rc = h.sdv_sample_truncated(n, V, stride, _dtype_code(logits), *common, *map(_addr, arrays), _addr(logits), n_samples,
+                                _addr(u), _addr(tokens), _addr(device_status), _stream(stream, logits.device))
     if rc != 0:
         raise SDVError(rc, "sdv_sample_truncated")
     return tokens, device_status
@@ -391,8 +400,8 @@ def truncate_rows(logits, temperature, *, top_k=0, top_p=1.0, min_p=0.0, V=None,
     if n_out != n or out.dtype != logits.dtype or out.device != logits.device:
         raise ValueError("out must have the logits' rows, type and device")
     device_status = _status(device_status, logits.device)
-    rc = h.sdv_truncate_rows(n, V, stride, _dtype_code(logits), *common, *map(_ptr, arrays), _ptr(logits), _ptr(out),
-                             out_stride, _ptr(device_status), _stream(stream, logits.device))
+    rc = h.sdv_truncate_rows(n, V, stride, _dtype_code(logits), *common, *map(_addr, arrays), _addr(logits), _addr(out),
+                             out_stride, _addr(device_status), _stream(stream, logits.device))
     if rc != 0:
         raise SDVError(rc, "sdv_truncate_rows")
     return out, device_status
@@ -414,8 +423,8 @@ def top_logits(logits, k, temperature=1.0, *, V=None, device_status=None, stream
     index = torch.empty((n, k), dtype=torch.int32, device=dev)
     rest = torch.empty(n, dtype=torch.float32, device=dev)
     device_status = _status(device_status, dev)
-    rc = h.sdv_top_logits(n, V, stride, _dtype_code(logits), float(temperature), _ptr(logits), k, _ptr(values),
-                          _ptr(index), _ptr(rest), _ptr(device_status), _stream(stream, dev))
+    rc = h.sdv_top_logits(n, V, stride, _dtype_code(logits), float(temperature), _addr(logits), k, _addr(values),
+                          _addr(index), _addr(rest), _addr(device_status), _stream(stream, dev))
     if rc != 0:
         raise SDVError(rc, "sdv_top_logits")
     return values, index, rest, device_status
@@ -444,9 +453,9 @@ def distill_forward(student, values, index, rest=None, *, temperature=1.0, row_w
                               or not stats.is_contiguous() or stats.device != student.device):
         raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
     device_status = _status(device_status, student.device)
-    rc = h.sdv_distill_forward(n, V, stride, _dtype_code(student), float(temperature), _ptr(student), values.shape[1],
-                               _dtype_code(values), _ptr(values), _ptr(index), _ptr(rest), _ptr(row_weight),
-                               _ptr(loss), _ptr(stats), _ptr(device_status), _stream(stream, student.device))
+    rc = h.sdv_distill_forward(n, V, stride, _dtype_code(student), float(temperature), _addr(student), values.shape[1],
+                               _dtype_code(values), _addr(values), _addr(index), _addr(rest), _addr(row_weight),
+                               _addr(loss), _addr(stats), _addr(device_status), _stream(stream, student.device))
     if rc != 0:
         raise SDVError(rc, "sdv_distill_forward")
     return loss, device_status
@@ -474,9 +483,9 @@ def distill_backward(student, values, index, rest, stats, grad_loss=None, *, tem
         raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
     _vector("grad_loss", grad_loss, n, torch.float32, student.device)
     grad, grad_stride = _grad_rows(student, grad, n, V)
-    rc = h.sdv_distill_backward(n, V, stride, _dtype_code(student), float(temperature), _ptr(student), values.shape[1],
-                                _dtype_code(values), _ptr(values), _ptr(index), _ptr(rest), _ptr(row_weight),
-                                _ptr(stats), _ptr(grad_loss), _ptr(grad), grad_stride,
+    rc = h.sdv_distill_backward(n, V, stride, _dtype_code(student), float(temperature), _addr(student), values.shape[1],
+                                _dtype_code(values), _addr(values), _addr(index), _addr(rest), _addr(row_weight),
+                                _addr(stats), _addr(grad_loss), _addr(grad), grad_stride,
                                 _stream(stream, student.device))
     if rc != 0:
         raise SDVError(rc, "sdv_distill_backward")
@@ -493,9 +502,9 @@ def distill_loss_grad(student, values, index, rest=None, *, temperature=1.0, row
     loss = torch.empty(n, dtype=torch.float32, device=student.device)
     grad, grad_stride = _grad_rows(student, grad, n, V)
     device_status = _status(device_status, student.device)
-    rc = h.sdv_distill_loss_grad(n, V, stride, _dtype_code(student), float(temperature), _ptr(student),
-                                 values.shape[1], _dtype_code(values), _ptr(values), _ptr(index), _ptr(rest),
-                                 _ptr(row_weight), _ptr(loss), _ptr(grad), grad_stride, _ptr(device_status),
+    rc = h.sdv_distill_loss_grad(n, V, stride, _dtype_code(student), float(temperature), _addr(student),
+                                 values.shape[1], _dtype_code(values), _addr(values), _addr(index), _addr(rest),
+                                 _addr(row_weight), _addr(loss), _addr(grad), grad_stride, _addr(device_status),
                                  _stream(stream, student.device))
     if rc != 0:
         raise SDVError(rc, "sdv_distill_loss_grad")

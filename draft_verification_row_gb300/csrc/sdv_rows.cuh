@@ -227,37 +227,66 @@ __device__ __forceinline__ u64 warp_scan_u64(u64 v, int lane)
     return v;
 }
 
+// Each lane below NT / 32 holds a warp's value: this warp's exclusive prefix
+// of them, and their total.
+template <int NT>
+__device__ __forceinline__ u64 across_warps(u64 mine, u64& total)
+{
+    constexpr int NW = NT / 32;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    u64 v = mine;
+#pragma unroll
+    for (int o = 1; o < NW; o <<= 1) {
+        const u64 n = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += n;
+    }
+    total = __shfl_sync(0xffffffffu, v, NW - 1);
+    return __shfl_sync(0xffffffffu, v - mine, w);
+}
+
 template <int NT>
 __device__ u64 block_sum(u64 v, BlockSmem<NT>& s)
 {
+    const int lane = threadIdx.x & 31;
     v = warp_sum_u64(v);
     __syncthreads();  // the last reader of part
-    if ((threadIdx.x & 31) == 0) s.part[threadIdx.x >> 5] = v;
+    if (lane == 0) s.part[threadIdx.x >> 5] = v;
     __syncthreads();
-    u64 t = 0;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) t += s.part[i];
-    return t;
+    u64 total;
+    across_warps<NT>(lane < NT / 32 ? s.part[lane] : 0, total);
+    return total;
 }
 
 // Sum over the threads before this one; total: over all of them.
 template <int NT>
 __device__ u64 block_scan(u64 v, u64& total, BlockSmem<NT>& s)
 {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     const u64 incl = warp_scan_u64(v, lane);
     __syncthreads();
-    if (lane == 31) s.part[w] = incl;
+    if (lane == 31) s.part[threadIdx.x >> 5] = incl;
     __syncthreads();
-    u64 before = 0, t = 0;
+    return across_warps<NT>(lane < NT / 32 ? s.part[lane] : 0, total) + incl - v;
+}
+
+// The same for sums below 2^32.
+template <int NT>
+__device__ uint32_t block_scan32(uint32_t v, uint32_t& total, BlockSmem<NT>& s)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t incl = v;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
-        const u64 p = s.part[i];
-        if (i < w) before += p;
-        t += p;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t n = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += n;
     }
-    total = t;
-    return before + incl - v;
+    uint32_t* const part = reinterpret_cast<uint32_t*>(s.part);
+    __syncthreads();
+    if (lane == 31) part[threadIdx.x >> 5] = incl;
+    __syncthreads();
+    const uint32_t p = lane < NT / 32 ? part[lane] : 0u;
+    total = __reduce_add_sync(0xffffffffu, p);
+    return __reduce_add_sync(0xffffffffu, lane < (int)(threadIdx.x >> 5) ? p : 0u) + incl - v;
 }
 
 template <int NT>
@@ -612,19 +641,15 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
     const int per = (g.n + NT / 32 - 1) / (NT / 32);
     const int g0 = min(w * per, g.n), g1 = min(g0 + per, g.n);
     int count = 0;
+#pragma unroll 4
     for (int i = g0 + lane; i < g1; i += 32) count += near(g.max[i]) ? 1 : 0;
-    count = __reduce_add_sync(0xffffffffu, count);
-    __syncthreads();
-    if (lane == 0) bs.part[w] = (u64)count;
+    uint32_t total_lines;
+    int at = (int)block_scan32<NT>((uint32_t)count, total_lines, bs);
+    at = __shfl_sync(0xffffffffu, at, 0);  // where this warp's begin
+    const int n_lines = (int)total_lines;
     if (tid == 0) bs.low = ~0u;
-    __syncthreads();
-    int at = 0, n_lines = 0;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
-        if (i < w) at += (int)bs.part[i];
-        n_lines += (int)bs.part[i];
-    }
     if (n_lines > cap) return n_lines;  // each has a near logit at least
+#pragma unroll 4
     for (int gb = g0; gb < g1; gb += 32) {
         const bool mine = gb + lane < g1 && near(g.max[gb + lane]);
         const unsigned mask = __ballot_sync(0xffffffffu, mine);
@@ -649,6 +674,7 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
         u64 counts = 0;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
+            if (p0 + i * NT + (tid & ~31) >= n_units) break;  // nothing in this warp
             float v[EPU];
             Elem<DT>::unpack(raw[i], v);
             uint32_t m = 0;
@@ -724,11 +750,10 @@ __device__ int bucket_of_kth(const Groups& g, float M, int k, Hist& h, BlockSmem
     __syncthreads();
     for (int i = tid; i < g.n; i += NT) atomicAdd(&h.lo[bucket_of(g.max[i], M)], 1u);
     __syncthreads();
-    uint32_t v[kPer], sum = 0;
+    uint32_t v[kPer], sum = 0, total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum += v[i] = h.lo[tid * kPer + i];
-    u64 total;
-    uint32_t run = (uint32_t)block_scan<NT>(sum, total, bs);
+    uint32_t run = block_scan32<NT>(sum, total, bs);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (run < (uint32_t)k && run + v[i] >= (uint32_t)k) bs.bucket = tid * kPer + i;

@@ -32,7 +32,7 @@ namespace {
 constexpr int kMaxSeg = (SDV_MAX_V / 4 + 1 + kSegU - 1) / kSegU;  // segments of the longest row
 constexpr int kListCap = 3072;                                    // listed tokens
 
-constexpr int kShort = 128;  // lists up to this length are ranked by counting
+constexpr int kShort = 256;  // lists up to this length are ranked by counting
 
 template <int NT>
 struct TruncSmem {
@@ -357,11 +357,10 @@ __device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncS
     }
     const u64 mass = block_sum<NT>((u64)(z * kOne), sm.bs);  // finer: every thread's share is cut off
     const u64 need = (u64)((float)mass * (p * 1.0001f) * (kStep / kOne)) + 1;
-    u64 v[kPer], sum = 0;
+    uint32_t v[kPer], sum = 0, total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum += v[i] = h.lo[tid * kPer + i];
-    u64 total;
-    u64 run = block_scan<NT>(sum, total, sm.bs);
+    u64 run = block_scan32<NT>(sum, total, sm.bs);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (run < need && run + v[i] >= need) sm.bs.bucket = tid * kPer + i;
@@ -399,7 +398,15 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
         l.top = bucket_of_kth<NT>(g, sc.M, st.k, sm.hist, sm.bs);
         if (st.p >= 1.f) l.top = min(l.top, bm);
     } else if (st.p < 1.f) {
-        l.top = min(bucket_of_share<NT>(g, st.p, sc, sm), bm);
+        l.top = bucket_of_share<NT>(g, st.p, sc, sm);
+        if (l.top == kFar) {
+            // the groups' largest tokens alone do not hold the share: as many
+            // tokens as a list has room for, if they are spread at random
+            // (n tokens then lie in G (1 - exp(-n / G)) of G groups)
+            const int some = (int)((float)g.n * (1.f - __expf(-0.8f * kListCap / (float)g.n)));
+            l.top = bucket_of_kth<NT>(g, sc.M, some, sm.hist, sm.bs);
+        }
+        l.top = min(l.top, bm);
     } else {
         l.top = bm;
     }
