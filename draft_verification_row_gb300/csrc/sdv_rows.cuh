@@ -23,6 +23,7 @@ struct Row {
     int off;  // elements before it in its first unit
     int V;
     int n_units;
+    const uint4* edge;  // the first and the last unit, in shared memory, once stage_edges has put them there
 };
 
 template <int DT>
@@ -34,6 +35,7 @@ __device__ __forceinline__ Row row_at(const void* base, long long r, long long s
     row.off = (int)(a & 15) / Elem<DT>::kBytes;
     row.V = V;
     row.n_units = (row.off + V + Elem<DT>::kPerUnit - 1) / Elem<DT>::kPerUnit;
+    row.edge = nullptr;
     return row;
 }
 
@@ -47,7 +49,7 @@ __device__ __forceinline__ bool whole_unit(const Row& row, int u)
 // A unit that the row's first or last element falls into: element by
 // element, so that nothing outside the row is read.
 template <int DT>
-__device__ __noinline__ uint4 edge_unit(const Row& row, int u)
+__device__ __forceinline__ uint4 edge_unit(const Row& row, int u)
 {
     constexpr int EPU = Elem<DT>::kPerUnit;
     uint32_t w[4];
@@ -68,11 +70,23 @@ __device__ __noinline__ uint4 edge_unit(const Row& row, int u)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The row's first and last unit in two words of shared memory, so that every
+// later read of any unit is one load without a branch around it (which would
+// keep a thread's loads from being in flight together).  Ends with a barrier.
+template <int DT>
+__device__ __forceinline__ void stage_edges(Row& row, uint4* edge)
+{
+    if (threadIdx.x < 2) edge[threadIdx.x] = edge_unit<DT>(row, threadIdx.x == 0 ? 0 : row.n_units - 1);
+    row.edge = edge;
+    __syncthreads();
+}
+
+// Unit u of a row with staged edges.
 template <int DT>
 __device__ __forceinline__ uint4 load_unit(const Row& row, int u)
 {
-    if (whole_unit<DT>(row, u)) return reinterpret_cast<const uint4*>(row.p)[u];
-    return edge_unit<DT>(row, u);
+    const uint4* const p = reinterpret_cast<const uint4*>(row.p) + u;
+    return *(whole_unit<DT>(row, u) ? p : row.edge + (u > 0 ? 1 : 0));
 }
 
 template <int DT>
@@ -399,28 +413,31 @@ __device__ Border find_border(const Src& src, bool mass, u64 need, uint32_t klo,
 // in shared memory by the one pass that reads the row from HBM.  The k-th
 // largest group maximum is a lower bound of the k-th largest logit, so what
 // follows reads only the lines whose maximum reaches it: about k of 2374
-// for a row of 151936 bf16 logits.  Rows of up to kUnitGroups units keep
-// every 16-byte unit's maximum instead (their k may come near the number of
-// lines).
+// for a row of 151936 bf16 logits.  Shorter rows have groups of 4, 2 or 1
+// units of 16 bytes, so that about 2000 groups are left for a k of 1000.
 
-constexpr int kUnitGroups = 8192;
 constexpr int kSegU = 256;  // units per segment: a warp's step of 8 per lane
 
-__host__ __device__ inline int units_bound(int V, int per_unit) { return (V + 2 * per_unit - 2) / per_unit; }
+__host__ __device__ inline int group_width(int n_units)
+{
+    return n_units <= 2048 ? 1 : n_units <= 4096 ? 2 : n_units <= 8192 ? 4 : 8;
+}
 
-// Groups of the longest row of V elements, at any alignment.
+// Room for the groups of a row of V elements, at any alignment (of which a
+// row may have one unit more, and so groups twice as wide): whole segments,
+// since a step writes all of its groups.
 __host__ __device__ inline int groups_bound(int V, int per_unit)
 {
-    const int u = units_bound(V, per_unit);
-    if ((V + per_unit - 1) / per_unit <= kUnitGroups) return u < kUnitGroups ? u : kUnitGroups;
-    return (u + kSegU - 1) / kSegU * (kSegU / 8);  // whole segments: a step writes all of its 32 lines
+    const int low = (V + per_unit - 1) / per_unit, high = (V + 2 * per_unit - 2) / per_unit;
+    const int n = (high + kSegU - 1) / kSegU * kSegU;
+    return n / group_width(low);
 }
 
 struct Groups {
     float* max;  // [n]
     float* sum;  // [n]: sum of 2^((x - max) c) over the group
     int n;
-    int width;  // units per group: 1 or 8
+    int shift;  // log2 of the units per group
 };
 
 template <int DT>
@@ -429,8 +446,9 @@ __device__ __forceinline__ Groups groups_of(const Row& row, float* max, float* s
     Groups g;
     g.max = max;
     g.sum = sum;
-    g.width = row.n_units <= kUnitGroups ? 1 : 8;
-    g.n = (row.n_units + g.width - 1) / g.width;
+    const int width = group_width(row.n_units);
+    g.shift = 31 - __clz(width);
+    g.n = (row.n_units + width - 1) >> g.shift;
     return g;
 }
 
@@ -512,25 +530,53 @@ __device__ __forceinline__ float unpacked_max(uint32_t a)
 }
 
 // Eight values per lane, value i belonging with those of the lane's
-// neighbours in its aligned eight lanes: lane j of the eight gets value j
-// reduced over them.  Seven exchanges in place of twenty-four.
-template <class T, class F>
-__device__ __forceinline__ T scatter_reduce(const T (&p)[8], int lane, F op)
+// neighbours in its aligned W lanes: each lane gets 8 / W of them reduced,
+// in r[0..]: values (lane % W) * (8 / W) + 0, 1, ...  For W = 8 that is
+// seven exchanges in place of twenty-four.
+template <int W, class T, class F>
+__device__ __forceinline__ void scatter_reduce(T (&r)[8], int lane, F op)
 {
-    T q[4], r[2];
-    const bool b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const T other = __shfl_xor_sync(0xffffffffu, b2 ? p[i] : p[i + 4], 4);
-        q[i] = op(b2 ? p[i + 4] : p[i], other);
-    }
+    for (int o = W / 2, left = 4; o > 0; o /= 2, left /= 2) {
+        const bool b = lane & o;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const T other = __shfl_xor_sync(0xffffffffu, b1 ? q[i] : q[i + 2], 2);
-        r[i] = op(b1 ? q[i + 2] : q[i], other);
+        for (int i = 0; i < 4; ++i) {
+            if (i >= left) break;
+            const T other = __shfl_xor_sync(0xffffffffu, b ? r[i] : r[i + left], o);
+            r[i] = op(b ? r[i + left] : r[i], other);
+        }
     }
-    const T other = __shfl_xor_sync(0xffffffffu, b0 ? r[0] : r[1], 1);
-    return op(b0 ? r[1] : r[0], other);
+}
+
+// One segment's groups of W units.
+template <int DT, int W, bool SUMS>
+__device__ __forceinline__ void scan_segment(const uint4 (&raw)[8], int s, int lane, const Groups& g, float c,
+                                             float& best)
+{
+    constexpr int kEach = 8 / W;  // groups a lane ends up with
+    uint32_t p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = packed_max<DT>(raw[i]);
+    scatter_reduce<W>(p, lane, [](uint32_t a, uint32_t b) { return larger<DT>(a, b); });
+    float m[kEach];
+    const int first = s * (kSegU / W) + lane / W, mine = lane % W * kEach;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        m[j] = unpacked_max<DT>(p[j]);
+        best = max_nan(best, m[j]);
+        g.max[first + (mine + j) * (32 / W)] = m[j];
+    }
+    if (SUMS) {
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float mi = W == 1 ? m[i % kEach] : __shfl_sync(0xffffffffu, m[i % kEach], (lane & -W) | i / kEach);
+            z[i] = mi > -INFINITY ? unit_sum<DT>(raw[i], c, mi) : 0.f;
+        }
+        scatter_reduce<W>(z, lane, [](float a, float b) { return a + b; });
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) g.sum[first + (mine + j) * (32 / W)] = z[j];
+    }
 }
 
 // Reads the row once: every group's maximum, and with SUMS its mass against
@@ -541,23 +587,6 @@ __device__ float scan_groups(const Row& row, const Groups& g, float c)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     float best = -INFINITY;
-    if (g.width == 1) {
-        constexpr int U = 4;
-        for (int u = threadIdx.x; u < row.n_units; u += U * NT) {
-            uint4 raw[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) raw[i] = load_unit_or_none<DT>(row, u + i * NT);
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                if (u + i * NT >= row.n_units) break;
-                const float m = Elem<DT>::unit_max(raw[i], -INFINITY);
-                best = max_nan(best, m);
-                g.max[u + i * NT] = m;
-                if (SUMS) g.sum[u + i * NT] = m > -INFINITY ? unit_sum<DT>(raw[i], c, m) : 0.f;
-            }
-        }
-        return best;
-    }
     const int n_seg = (row.n_units + kSegU - 1) / kSegU;
     for (int s = w; s < n_seg; s += NT / 32) {
         const int u = s * kSegU + lane;
@@ -570,23 +599,14 @@ __device__ float scan_groups(const Row& row, const Groups& g, float c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) raw[i] = load_unit_or_none<DT>(row, u + i * 32);
         }
-        uint32_t p[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = packed_max<DT>(raw[i]);
-        const float m = unpacked_max<DT>(
-            scatter_reduce(p, lane, [](uint32_t a, uint32_t b) { return larger<DT>(a, b); }));
-        best = max_nan(best, m);
-        const int line = s * 32 + (lane & 7) * 4 + (lane >> 3);
-        g.max[line] = m;
-        if (SUMS) {
-            float z[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float mi = __shfl_sync(0xffffffffu, m, (lane & 24) | i);
-                z[i] = mi > -INFINITY ? unit_sum<DT>(raw[i], c, mi) : 0.f;
-            }
-            g.sum[line] = scatter_reduce(z, lane, [](float a, float b) { return a + b; });
-        }
+        if (g.shift == 3)
+            scan_segment<DT, 8, SUMS>(raw, s, lane, g, c, best);
+        else if (g.shift == 2)
+            scan_segment<DT, 4, SUMS>(raw, s, lane, g, c, best);
+        else if (g.shift == 1)
+            scan_segment<DT, 2, SUMS>(raw, s, lane, g, c, best);
+        else
+            scan_segment<DT, 1, SUMS>(raw, s, lane, g, c, best);
     }
     return best;
 }
@@ -657,7 +677,7 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
         at += __popc(mask);
     }
     __syncthreads();
-    const int n_units = n_lines * g.width;
+    const int n_units = n_lines << g.shift, in_group = (1 << g.shift) - 1;
     int n = 0;
     uint32_t low = ~0u;
     for (int p0 = 0; p0 < n_units; p0 += U * NT) {
@@ -666,7 +686,7 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int p = p0 + i * NT + tid;
-            unit[i] = p >= n_units ? -1 : g.width == 1 ? lines[p] : lines[p >> 3] * 8 + (p & 7);
+            unit[i] = p >= n_units ? -1 : (lines[p >> g.shift] << g.shift) + (p & in_group);
             if (unit[i] >= row.n_units) unit[i] = -1;
             raw[i] = unit[i] >= 0 ? load_unit<DT>(row, unit[i]) : no_unit<DT>();
         }
@@ -686,23 +706,24 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
         }
         u64 total;
         u64 before = block_scan<NT>(counts, total, bs);
+        // by set marks, few of a warp's 1024: the element is read again (its
+        // line is in L1), since registers cannot be indexed
+        int first[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const uint32_t m = marks >> (8 * i) & 0xffu;
-            int to = n + (int)(before >> (16 * i) & 0xffffu);
-            if (m) {
-                float v[EPU];
-                Elem<DT>::unpack(raw[i], v);
-#pragma unroll
-                for (int e = 0; e < EPU; ++e) {
-                    if (!(m >> e & 1)) continue;
-                    const uint32_t k = key_of<DT>(v[e]);
-                    low = min(low, k);
-                    if (to < cap) list[to] = list_entry(k, unit[i] * EPU + e - row.off);
-                    ++to;
-                }
-            }
+            first[i] = n + (int)(before >> (16 * i) & 0xffffu);
             n += (int)(total >> (16 * i) & 0xffffu);
+        }
+        while (marks) {
+            const int b = __ffs(marks) - 1, i = b >> 3;
+            marks &= marks - 1;
+            const int u = i == 0 ? unit[0] : i == 1 ? unit[1] : i == 2 ? unit[2] : unit[3];
+            int& to = i == 0 ? first[0] : i == 1 ? first[1] : i == 2 ? first[2] : first[3];
+            const int x = u * EPU + (b & 7) - row.off;
+            const uint32_t k = key_of<DT>(load_elem<DT>(row, x));
+            low = min(low, k);
+            if (to < cap) list[to] = list_entry(k, x);
+            ++to;
         }
     }
     low = __reduce_min_sync(0xffffffffu, low);
@@ -712,29 +733,26 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
     return n;
 }
 
-// One entry of a list of up to NT tokens, in a thread of its own: how many
-// tokens come before it in the descending order and, with MASS, their mass
-// (w: each token's weight).  weights: NT words of scratch.
-template <int NT, bool MASS>
-__device__ __forceinline__ void rank_of(const u64* list, int n, u64 mine, u64 w, u64* weights, int& rank, u64& before)
+// One entry of a list of up to NT tokens in index order, in a thread of its
+// own: how many of them come before it in the descending order.  Tokens
+// listed earlier win ties, so those compare with >=, later ones with >.
+__device__ __forceinline__ int rank_of(const u64* list, int n, int i)
 {
-    if (MASS) {
-        __syncthreads();
-        if ((int)threadIdx.x < n) weights[threadIdx.x] = w;
-        __syncthreads();
+    const int base = i & ~31;
+    if (base >= n) return 0;
+    const uint32_t key = i < n ? entry_key(list[i]) : 0u;
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < base; ++j) rank += entry_key(list[j]) >= key ? 1 : 0;
+    const int end = min(base + 32, n);
+#pragma unroll 8
+    for (int j = base; j < end; ++j) {
+        const uint32_t k = entry_key(list[j]);
+        rank += k > key || (k == key && j < i) ? 1 : 0;
     }
-    rank = 0;
-    before = 0;
-    if ((int)(threadIdx.x & ~31) >= n) return;
-    // descending keys, then ascending indexes, as one ascending number
-    const u64 order = mine ^ 0xffffffff00000000ull;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-        if ((list[j] ^ 0xffffffff00000000ull) < order) {
-            ++rank;
-            if (MASS) before += weights[j];
-        }
-    }
+#pragma unroll 8
+    for (int j = end; j < n; ++j) rank += entry_key(list[j]) > key ? 1 : 0;
+    return rank;
 }
 
 // The bucket by which k groups have their maximum: at least k tokens lie in

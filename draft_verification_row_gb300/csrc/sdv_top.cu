@@ -41,6 +41,7 @@ struct TopSmem {
     Hist hist;
     u64 list[SDV_MAX_TOP];  // ~key << 32 | index: ascending is the row's descending order
     float part[NT / 32];
+    uint4 edge[2];
 };
 
 // Ascending bitonic sort of n (a power of two) entries in shared memory.
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int group
     __shared__ TopSmem<NT> sm;
     extern __shared__ u64 cand[];  // [kTopList], then the groups' maxima and sums
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const Row row = row_at<DT>(a.logits, r, a.stride, a.V);
+    Row row = row_at<DT>(a.logits, r, a.stride, a.V);
+    stage_edges<DT>(row, sm.edge);
     float* const gmax = reinterpret_cast<float*>(cand + kTopList);
     const Groups g = groups_of<DT>(row, gmax, gmax + groups);
     const float c = (float)a.c;
@@ -192,10 +194,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int group
         s.z = 0.f;
     }
     if (n <= NT) {  // a token in each thread: its place is the number of those before it
-        int rank;
-        u64 before;
         const u64 e = tid < n ? cand[tid] : 0;
-        rank_of<NT, false>(cand, n, e, 0, nullptr, rank, before);
+        const int rank = rank_of(cand, n, tid);
         const float x = key_value<DT>(entry_key(e));
         if (tid < n && rank < a.k) put<DT>(a, o + rank, x, entry_index(e));
         if (tid < n && rank >= a.k) s.add(x, 1.f, c);

@@ -42,6 +42,7 @@ struct TruncSmem {
     u64 seg[kMaxSeg];  // per segment: tied tokens, then kept mass
     int last;          // index of the last kept token of the border's key
     float2 min_p_off;  // T ln(min_p)
+    uint4 edge[2];
 };
 
 // The elements of a row, by threads: unit tid, tid + NT, ...
@@ -334,7 +335,7 @@ __device__ __forceinline__ float light_weight(float x, const Scale& sc)
 constexpr float kOne = (float)(1ull << kWeightBits);
 
 // The bucket by which the groups' largest weights alone sum to the share p
-// of the row's mass: the tokens in buckets 0 to it have at least that mass,
+// of the row's mass (and each group's sum against the row's maximum): the tokens in buckets 0 to it have at least that mass,
 // up to the rounding of the fp32 sums.  kFar: they do not.
 template <int NT>
 __device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncSmem<NT>& sm)
@@ -349,9 +350,9 @@ __device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncS
     __syncthreads();
     float z = 0.f;
     for (int i = tid; i < g.n; i += NT) {
-        const float w = light_weight(g.max[i], sc);
-        if (w == 0.f) continue;
-        z += g.sum[i] * w;
+        const float w = light_weight(g.max[i], sc), zi = w > 0.f ? g.sum[i] * w : 0.f;
+        g.sum[i] = zi;
+        z += zi;
         const uint32_t v = (uint32_t)(w * kStep);
         if (v) atomicAdd(&h.lo[bucket_of(g.max[i], sc.M)], v);
     }
@@ -415,27 +416,24 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
     float rest = 0.f;
     l.n = collect<DT, NT>(row, g, Near(sc.M, l.top), l.at, kListCap, l.low, sm.hist, sm.bs,
                           [&](const uint4& raw, uint32_t marks) {
-                              if (!sums) return;
-                              float v[Elem<DT>::kPerUnit];
-                              Elem<DT>::unpack(raw, v);
-#pragma unroll
-                              for (int e = 0; e < Elem<DT>::kPerUnit; ++e)
-                                  if (!(marks >> e & 1)) rest += light_weight(v[e], sc);
+                              if (sums) rest += unit_sum<DT>(without<DT>(raw, marks), sc.ch, sc.M);
                           });
     l.rest = rest;
     return l.n <= kListCap;
 }
 
-// The mass of what is not listed, in fp32 sums, each weight within 2^-18
-// (ex2.approx 2^-22, an exponent of up to 46 rounded in three places, sums
-// of up to 64 terms), and the bound on its error; or, where that leaves a
+// The mass of what is not listed, in fp32 sums (bucket_of_share has taken the
+// groups' sums against M), each weight within 2^-18 (ex2.approx 2^-22, an
+// exponent of up to 46 rounded in three places, sums of up to 64 terms), and
+// the bound on its error; or, where that leaves a
 // border open, in fixed point from the row.
 template <int NT>
 __device__ u64 light_rest(const Groups& g, const List& l, const Scale& sc, u64& error, BlockSmem<NT>& bs)
 {
     float rest = l.rest;
+    const Near near(sc.M, l.top);
     for (int i = threadIdx.x; i < g.n; i += NT)
-        if (bucket_of(g.max[i], sc.M) > l.top) rest += g.sum[i] * light_weight(g.max[i], sc);
+        if (!near(g.max[i])) rest += g.sum[i];
     const u64 other = block_sum<NT>((u64)(rest * kOne), bs);
     error = (other >> 18) + 64 * NT;
     return other;
@@ -516,27 +514,34 @@ __device__ bool list_kept(const Row& row, const Groups& g, const Settings& st, c
     return true;
 }
 
-// The kept set of a short list, one token in each thread: the tokens
-// before each one and their mass are counted directly, and a token is kept
-// if they number less than top_k and weigh less than the share top_p.
-// Returns 1 where this thread's token is kept (w: its weight), 0 where not,
-// -1 (in all threads) where the kept set is not within the list.
+// The kept set of a short list, one token in each thread.  Every token's
+// place in the descending order is counted, the weights are laid out in that
+// order and summed up, and the kept tokens are those whose place is below
+// top_k, whose earlier tokens weigh less than the share top_p, and which
+// min_p keeps: a prefix, whose length is counted.  Returns 1 where this
+// thread's token is kept (w: its weight), 0 where not, -1 (in all threads)
+// where the kept set is not within the list.
 template <int DT, int NT>
 __device__ int short_kept(const Row& row, const Groups& g, const Settings& st, const Scale& sc, float xm,
                           const List& l, u64& w, TruncSmem<NT>& sm)
 {
-    const bool mine = (int)threadIdx.x < l.n;
-    const u64 e = mine ? l.at[threadIdx.x] : 0;
-    const float x = key_value<DT>(entry_key(e));
-    const bool by_count = st.k > 0 && st.k < row.V;
+    const int tid = threadIdx.x;
+    const bool mine = tid < l.n;
+    const float x = mine ? key_value<DT>(entry_key(l.at[tid])) : -INFINITY;
+    const int rank = rank_of(l.at, l.n, tid);
     w = !mine ? 0 : st.T > 0.f ? weight_of(x, sc, sm.table) : 1;
-    int rank;
-    u64 before;
-    rank_of<NT, true>(l.at, l.n, e, w, reinterpret_cast<u64*>(&sm.hist), rank, before);
     if (st.T == 0.f) return mine && rank == 0;
-    bool kept = mine && (!by_count || rank < st.k);
+    const bool by_count = st.k > 0 && st.k < row.V;
+    const int limit = by_count ? min(st.k, l.n) : l.n;
+    int n = limit;
     if (st.p < 1.f) {
-        const u64 listed = block_sum<NT>(kept ? w : 0, sm.bs);
+        // in this thread from here on: the token of rank tid
+        u64* const sorted = reinterpret_cast<u64*>(&sm.hist);
+        __syncthreads();
+        if (mine) sorted[rank] = w;
+        __syncthreads();
+        u64 listed;
+        const u64 before = block_scan<NT>(tid < limit ? sorted[tid] : 0, listed, sm.bs);
         u64 other = 0, error = 0;
         if (!by_count && !l.whole) other = light_rest<NT>(g, l, sc, error, sm.bs);
         for (;;) {
@@ -545,17 +550,15 @@ __device__ int short_kept(const Row& row, const Groups& g, const Settings& st, c
                 if (!l.ends) return -1;
                 break;
             }
+            n = __syncthreads_count(tid < limit && before < lo);
+            if (error == 0) break;
             const u64 hi = share_of(st.p, listed + other + error);
-            const bool in = kept && before < lo;
-            if (error == 0 || !__syncthreads_or(hi > listed || (kept && before < hi) != in)) {
-                kept = in;
-                break;
-            }
+            if (hi <= listed && n == __syncthreads_count(tid < limit && before < hi)) break;
             other = exact_rest<DT, NT>(row, l, sc, sm.table, sm.bs);
             error = 0;
         }
     }
-    return kept && x >= xm;
+    return mine && rank < n && x >= xm;
 }
 
 __device__ __forceinline__ bool entry_kept(u64 e, const Kept& c)
@@ -701,7 +704,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
     const int r = blockIdx.x;
     const int tid = threadIdx.x;
     for (int i = tid; i < 64; i += NT) sm.table[i] = kExp2Table[i];
-    const Row row = row_at<DT>(a.logits, r, a.stride, a.V);
+    Row row = row_at<DT>(a.logits, r, a.stride, a.V);
+    stage_edges<DT>(row, sm.edge);
     const Settings st = settings_of(a, r);
     Scale sc;
     set_scale(sc, st.ok ? st.T : 0.f);
