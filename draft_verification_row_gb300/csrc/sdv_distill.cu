@@ -125,10 +125,10 @@ __device__ void fill_row(const Row& g, float x)
 enum { DISTILL_FORWARD = 0, DISTILL_BACKWARD = 1, DISTILL_BOTH = 2 };
 
 constexpr size_t kCacheBytes = 48 << 10;
-constexpr int kUnroll = 4;  // units a thread has in flight
 
-template <int DT, int NT, int MODE>
-__global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
+// kUnroll: units a thread has in flight; PER_SM: CTAs on an SM.
+template <int DT, int NT, int kUnroll, int PER_SM, int MODE>
+__global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
 {
     using E = Elem<DT>;
     constexpr int EPU = E::kPerUnit;
@@ -316,26 +316,40 @@ __global__ void __launch_bounds__(NT, 1536 / NT) distill_kernel(DistillArgs a)
     }
 }
 
-template <int DT, int MODE>
-cudaError_t launch(DistillArgs a, cudaStream_t st)
+template <int DT, int NT, int U, int PER_SM, int MODE>
+cudaError_t launch(DistillArgs a, bool cache, cudaStream_t st)
 {
-    constexpr int NT = 512;
     // the bitmap, by element position from the row's first 16-byte boundary
     const size_t bits = MODE == DISTILL_BACKWARD ? 0 : ((size_t)a.V + 2 * Elem<DT>::kPerUnit + 31) / 32 * 4;
     a.cached = 0;
-    if (MODE == DISTILL_BOTH) {
-        const size_t units = (size_t)a.V / Elem<DT>::kPerUnit + 2;
-        const size_t room = kCacheBytes / 16;
+    if (cache) {
+        const size_t units = (size_t)a.V / Elem<DT>::kPerUnit + 2, room = kCacheBytes / 16;
         a.cached = (int)(units < room ? units : room);
     }
     const size_t smem = (size_t)a.cached * 16 + bits;
-    auto* kernel = distill_kernel<DT, NT, MODE>;
-    if (MODE == DISTILL_BOTH) {
+    auto* kernel = distill_kernel<DT, NT, U, PER_SM, MODE>;
+    if (cache) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
     kernel<<<a.n_rows, NT, smem, st>>>(a);
     return cudaGetLastError();
+}
+
+// CTA shapes (8192 rows of 151936 bf16 unless stated).  Loss and gradient:
+// the second pass finds the row in L2 only while few rows are in flight.
+// Long rows: 304 CTAs of 512 threads, 48 KB of each row kept in shared
+// memory: 942 us; 456 CTAs 1090 us, 912 CTAs of 256 threads 1049 us (with
+// 96 KB kept, 1142 us).  Rows of up to 96 KB: many small CTAs, whose fixed
+// work per row overlaps better: 1000 x 20011 fp32 41 us against 48 us.  The
+// loss alone, 512 x 128256 bf16: 31 us against 35 us.
+template <int DT, int MODE>
+cudaError_t launch(const DistillArgs& a, cudaStream_t st)
+{
+    if (MODE == DISTILL_FORWARD) return launch<DT, 256, 8, 4, MODE>(a, false, st);
+    if (MODE == DISTILL_BOTH && (size_t)a.V * Elem<DT>::kBytes > (96 << 10))
+        return launch<DT, 512, 8, 2, MODE>(a, true, st);
+    return launch<DT, 256, 4, 6, MODE>(a, false, st);
 }
 
 template <int DT>
