@@ -416,7 +416,8 @@ __device__ Border find_border(const Src& src, bool mass, u64 need, uint32_t klo,
 // for a row of 151936 bf16 logits.  Shorter rows have groups of 4, 2 or 1
 // units of 16 bytes, so that about 2000 groups are left for a k of 1000.
 
-constexpr int kSegU = 256;  // units per segment: a warp's step of 8 per lane
+constexpr int kLaneU = 8;              // units a lane has in flight
+constexpr int kSegU = 32 * kLaneU;     // units per segment: a warp's step
 
 __host__ __device__ inline int group_width(int n_units)
 {
@@ -440,13 +441,16 @@ struct Groups {
     int shift;  // log2 of the units per group
 };
 
+// room: floats at max and at sum; finer: no sums are taken, and the maxima of
+// groups half as wide fill both.
 template <int DT>
-__device__ __forceinline__ Groups groups_of(const Row& row, float* max, float* sum)
+__device__ __forceinline__ Groups groups_of(const Row& row, float* max, int room, bool finer)
 {
     Groups g;
     g.max = max;
-    g.sum = sum;
-    const int width = group_width(row.n_units);
+    g.sum = max + room;
+    int width = group_width(row.n_units);
+    if (finer && width > 1) width /= 2;
     g.shift = 31 - __clz(width);
     g.n = (row.n_units + width - 1) >> g.shift;
     return g;
@@ -529,18 +533,29 @@ __device__ __forceinline__ float unpacked_max(uint32_t a)
     return max_nan(bf_lo(a), bf_hi(a));
 }
 
-// Eight values per lane, value i belonging with those of the lane's
-// neighbours in its aligned W lanes: each lane gets 8 / W of them reduced,
-// in r[0..]: values (lane % W) * (8 / W) + 0, 1, ...  For W = 8 that is
-// seven exchanges in place of twenty-four.
-template <int W, class T, class F>
-__device__ __forceinline__ void scatter_reduce(T (&r)[8], int lane, F op)
+// N values per lane, value i belonging with those of the lane's neighbours in
+// its aligned W lanes: each lane gets kEach = max(1, N / W) of them reduced,
+// in r[0..]: those from (lane % W) / kShare * kEach on, where kShare lanes
+// hold the same.  For N = W = 8 that is seven exchanges in place of
+// twenty-four.
+template <int N, int W>
+struct Scatter {
+    static constexpr int kEach = N / W > 1 ? N / W : 1;
+    static constexpr int kShare = W * kEach / N;
+};
+
+template <int N, int W, class T, class F>
+__device__ __forceinline__ void scatter_reduce(T (&r)[N], int lane, F op)
 {
 #pragma unroll
-    for (int o = W / 2, left = 4; o > 0; o /= 2, left /= 2) {
+    for (int o = W / 2, left = N / 2; o > 0; o /= 2, left /= 2) {
         const bool b = lane & o;
+        if (left == 0) {
+            r[0] = op(r[0], __shfl_xor_sync(0xffffffffu, r[0], o));
+            continue;
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < N / 2; ++i) {
             if (i >= left) break;
             const T other = __shfl_xor_sync(0xffffffffu, b ? r[i] : r[i + left], o);
             r[i] = op(b ? r[i + left] : r[i], other);
@@ -550,16 +565,17 @@ __device__ __forceinline__ void scatter_reduce(T (&r)[8], int lane, F op)
 
 // One segment's groups of W units.
 template <int DT, int W, bool SUMS>
-__device__ __forceinline__ void scan_segment(const uint4 (&raw)[8], int s, int lane, const Groups& g, float c,
+__device__ __forceinline__ void scan_segment(const uint4 (&raw)[kLaneU], int s, int lane, const Groups& g, float c,
                                              float& best)
 {
-    constexpr int kEach = 8 / W;  // groups a lane ends up with
-    uint32_t p[8];
+    using Sc = Scatter<kLaneU, W>;
+    constexpr int kEach = Sc::kEach;
+    uint32_t p[kLaneU];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = packed_max<DT>(raw[i]);
-    scatter_reduce<W>(p, lane, [](uint32_t a, uint32_t b) { return larger<DT>(a, b); });
+    for (int i = 0; i < kLaneU; ++i) p[i] = packed_max<DT>(raw[i]);
+    scatter_reduce<kLaneU, W>(p, lane, [](uint32_t a, uint32_t b) { return larger<DT>(a, b); });
     float m[kEach];
-    const int first = s * (kSegU / W) + lane / W, mine = lane % W * kEach;
+    const int first = s * (kSegU / W) + lane / W, mine = lane % W / Sc::kShare * kEach;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         m[j] = unpacked_max<DT>(p[j]);
@@ -567,13 +583,14 @@ __device__ __forceinline__ void scan_segment(const uint4 (&raw)[8], int s, int l
         g.max[first + (mine + j) * (32 / W)] = m[j];
     }
     if (SUMS) {
-        float z[8];
+        float z[kLaneU];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float mi = W == 1 ? m[i % kEach] : __shfl_sync(0xffffffffu, m[i % kEach], (lane & -W) | i / kEach);
+        for (int i = 0; i < kLaneU; ++i) {
+            const float mi = W == 1 ? m[i % kEach]
+                                    : __shfl_sync(0xffffffffu, m[i % kEach], (lane & -W) | i / kEach * Sc::kShare);
             z[i] = mi > -INFINITY ? unit_sum<DT>(raw[i], c, mi) : 0.f;
         }
-        scatter_reduce<W>(z, lane, [](float a, float b) { return a + b; });
+        scatter_reduce<kLaneU, W>(z, lane, [](float a, float b) { return a + b; });
 #pragma unroll
         for (int j = 0; j < kEach; ++j) g.sum[first + (mine + j) * (32 / W)] = z[j];
     }
@@ -590,14 +607,14 @@ __device__ float scan_groups(const Row& row, const Groups& g, float c)
     const int n_seg = (row.n_units + kSegU - 1) / kSegU;
     for (int s = w; s < n_seg; s += NT / 32) {
         const int u = s * kSegU + lane;
-        uint4 raw[8];
+        uint4 raw[kLaneU];
         if (s > 0 && s + 1 < n_seg) {
             const uint4* p = reinterpret_cast<const uint4*>(row.p) + u;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) raw[i] = p[i * 32];
+            for (int i = 0; i < kLaneU; ++i) raw[i] = p[i * 32];
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) raw[i] = load_unit_or_none<DT>(row, u + i * 32);
+            for (int i = 0; i < kLaneU; ++i) raw[i] = load_unit_or_none<DT>(row, u + i * 32);
         }
         if (g.shift == 3)
             scan_segment<DT, 8, SUMS>(raw, s, lane, g, c, best);
@@ -643,9 +660,11 @@ __device__ __forceinline__ u64 list_entry(uint32_t key, int x) { return (u64)key
 __device__ __forceinline__ uint32_t entry_key(u64 e) { return (uint32_t)(e >> 32); }
 __device__ __forceinline__ int entry_index(u64 e) { return (int)(uint32_t)e; }
 
+constexpr int kMaxLines = (int)(sizeof(Hist) / sizeof(uint16_t));
+
 // The logits of a row that are near (all threads), listed in index order;
-// returns how many there are, more than cap (<= 2 kBuckets * 2) where they
-// were not all listed, and the lowest listed key.  other(raw, marks): is
+// returns how many there are, more than cap where they were not all listed,
+// and the lowest listed key.  other(raw, marks): is
 // called for each unit of the lines read, with the marks of its listed
 // elements.  The lines' loads are all in flight together, so this waits for
 // L2 once (per 4 NT units); sums over four units a thread go through one
@@ -668,7 +687,7 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
     at = __shfl_sync(0xffffffffu, at, 0);  // where this warp's begin
     const int n_lines = (int)total_lines;
     if (tid == 0) bs.low = ~0u;
-    if (n_lines > cap) return n_lines;  // each has a near logit at least
+    if (n_lines > cap || n_lines > kMaxLines) return cap + 1;  // each has a near logit at least
 #pragma unroll 4
     for (int gb = g0; gb < g1; gb += 32) {
         const bool mine = gb + lane < g1 && near(g.max[gb + lane]);
@@ -680,7 +699,7 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
     const int n_units = n_lines << g.shift, in_group = (1 << g.shift) - 1;
     int n = 0;
     uint32_t low = ~0u;
-    for (int p0 = 0; p0 < n_units; p0 += U * NT) {
+    for (int p0 = 0; p0 < n_units && n <= cap; p0 += U * NT) {
         uint4 raw[U];
         int unit[U];
 #pragma unroll

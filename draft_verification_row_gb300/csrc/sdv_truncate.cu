@@ -30,9 +30,14 @@ namespace sdv {
 namespace {
 
 constexpr int kMaxSeg = (SDV_MAX_V / 4 + 1 + kSegU - 1) / kSegU;  // segments of the longest row
-constexpr int kListCap = 3072;                                    // listed tokens
+constexpr int kListCap = 8192;                                    // listed tokens
+constexpr int kWhole = 3072;                                      // rows up to this length are listed whole
 
 constexpr int kShort = 256;  // lists up to this length are ranked by counting
+
+struct Band {  // buckets
+    int lo, hi;
+};
 
 template <int NT>
 struct TruncSmem {
@@ -41,6 +46,8 @@ struct TruncSmem {
     u64 table[64];
     u64 seg[kMaxSeg];  // per segment: tied tokens, then kept mass
     int last;          // index of the last kept token of the border's key
+    int count;         // band_kept: the band's tokens
+    Band band;
     float2 min_p_off;  // T ln(min_p)
     uint4 edge[2];
 };
@@ -336,9 +343,10 @@ constexpr float kOne = (float)(1ull << kWeightBits);
 
 // The bucket by which the groups' largest weights alone sum to the share p
 // of the row's mass (and each group's sum against the row's maximum): the tokens in buckets 0 to it have at least that mass,
-// up to the rounding of the fp32 sums.  kFar: they do not.
+// up to the rounding of the fp32 sums.  kFar: they do not; near_miss: but
+// they hold most of it.
 template <int NT>
-__device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncSmem<NT>& sm)
+__device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncSmem<NT>& sm, bool& near_miss)
 {
     constexpr int kPer = kBuckets / NT;
     constexpr float kStep = 262144.f;  // 8192 groups of weight 1 stay below 2^31
@@ -368,7 +376,176 @@ __device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncS
         run += v[i];
     }
     __syncthreads();
+    near_miss = (float)total >= 0.88f * (float)need;
     return sm.bs.bucket;
+}
+
+// ------------------------------------------------------------------------
+// top_p of rows whose kept set no list can hold
+
+// What the row's tokens weigh by buckets, in fp32 up to 2^-13: a count of
+// 2^-13 shares of the bucket's largest weight, which 32 bits hold for any
+// row.  Then the buckets in which the share p of the row's mass may be
+// reached, as far as these sums can tell.
+__device__ __forceinline__ float bucket_exponent(int b, float c)
+{
+    // the least distance in bucket b, as an exponent, rounded down
+    const float t = b == 0 ? 0.f : __uint_as_float((uint32_t)(b + ((127 - 13) << 5)) << 18);
+    return floorf(t * c);
+}
+
+template <int DT, int NT>
+__device__ Band band_of_share(const Row& row, float p, const Scale& sc, TruncSmem<NT>& sm)
+{
+    constexpr int kPer = kBuckets / NT;
+    constexpr float kUnit = 8192.f;
+    const int tid = threadIdx.x;
+    __syncthreads();
+    for (int i = tid; i < kBuckets; i += NT) sm.hist.lo[i] = 0u;
+    if (tid == 0) sm.band = {kFar, -1};
+    __syncthreads();
+    const RowSource<DT, NT> src{row};
+    src.each([&](float x) {
+        const float d = x - sc.M;
+        if (!(d * sc.ch >= -60.f)) return;  // 2^18 of these are nothing
+        const int b = bucket_of(x, sc.M);
+        atomicAdd(&sm.hist.lo[b], __float2uint_rn(ex2(fmaf(d, sc.ch, bucket_exponent(b, sc.ch))) * kUnit));
+    });
+    __syncthreads();
+    u64 v[kPer], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int b = tid * kPer + i;
+        const float n = (float)sm.hist.lo[b];
+        v[i] = n > 0.f ? (u64)(n * ex2(-bucket_exponent(b, sc.ch)) * (kOne / kUnit)) : 0;
+        sum += v[i];
+    }
+    const u64 before = block_scan<NT>(sum, total, sm.bs);
+    const float share = p * (float)total;
+    const u64 lo = (u64)(share * (1.f - 4e-4f)), hi = (u64)(share * (1.f + 4e-4f)) + 1;
+    u64 run = before;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (run <= lo && run + v[i] > lo) sm.band.lo = tid * kPer + i;
+        if (run < hi && run + v[i] >= hi) sm.band.hi = tid * kPer + i;
+        run += v[i];
+    }
+    __syncthreads();
+    return sm.band;
+}
+
+// The kept set of such a row: one pass in fixed point takes the mass above
+// the band by segments (seg), the band's tokens into the list, in any order,
+// and the rest's mass; the border is then searched in the list.  False: it
+// is not in the band, or the band is too long.  seg holds the kept mass of
+// the row's segments afterwards, unless min_p ends the kept set earlier
+// (seg_valid).
+template <int DT, int NT>
+__device__ bool band_kept(const Row& row, const Settings& st, const Scale& sc, float xm, u64* list, TruncSmem<NT>& sm,
+                          Kept& kept, bool& seg_valid)
+{
+    constexpr int EPU = Elem<DT>::kPerUnit;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const Band band = band_of_share<DT, NT>(row, st.p, sc, sm);
+    if (band.lo > band.hi || band.hi >= kFar) return false;
+    const Near above(sc.M, band.lo - 1), within(sc.M, band.hi);
+    if (tid == 0) sm.count = 0;
+    __syncthreads();
+    const int n_seg = (row.n_units + kSegU - 1) / kSegU;
+    u64 high = 0, low = 0;
+    for (int s = w; s < n_seg; s += NT / 32) {
+        u64 mine = 0;
+        for (int u = s * kSegU + lane; u < min((s + 1) * kSegU, row.n_units); u += 32) {
+            float v[EPU];
+            load_elems<DT>(row, u, v);
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) {
+                const u64 wt = weight_of(v[e], sc, sm.table);
+                if (band.lo > 0 && above(v[e]))
+                    mine += wt;
+                else if (!within(v[e]))
+                    low += wt;
+                else {
+                    const int at = atomicAdd(&sm.count, 1);
+                    if (at < kListCap) list[at] = list_entry(key_of<DT>(v[e]), u * EPU + e - row.off);
+                }
+            }
+        }
+        mine = warp_sum_u64(mine);
+        if (lane == 0) {
+            sm.seg[s] = mine;
+            high += mine;
+        }
+    }
+    high = block_sum<NT>(high, sm.bs);
+    low = block_sum<NT>(low, sm.bs);
+    const int n = sm.count;
+    if (n > kListCap || n == 0) return false;
+    const ListSource<DT, NT> src{list, n};
+    u64 mid = 0;
+    src.each([&](float x) { mid += weight_of(x, sc, sm.table); });
+    mid = block_sum<NT>(mid, sm.bs);
+    const u64 need = share_of(st.p, high + mid + low);
+    if (need <= high || need > high + mid) return false;
+    uint32_t klo = ~0u, khi = 0u;
+    for (int i = tid; i < n; i += NT) {
+        klo = min(klo, entry_key(list[i]));
+        khi = max(khi, entry_key(list[i]));
+    }
+    klo = __reduce_min_sync(0xffffffffu, klo);
+    khi = __reduce_max_sync(0xffffffffu, khi);
+    __syncthreads();
+    if (lane == 0) sm.bs.part[w] = (u64)khi << 32 | klo;
+    __syncthreads();
+    for (int i = 0; i < NT / 32; ++i) {
+        klo = min(klo, (uint32_t)sm.bs.part[i]);
+        khi = max(khi, (uint32_t)(sm.bs.part[i] >> 32));
+    }
+    const Border b = find_border<DT, NT>(src, true, need - high, klo, khi, sc, sm.table, sm.hist, sm.bs);
+    const u64 wk = weight_of(key_value<DT>(b.key), sc, sm.table);
+    Cut c = {b.key, (need - high - b.above + wk - 1) / wk};
+    seg_valid = true;
+    if (xm > -INFINITY) {
+        cut_at_logit<DT>(xm, c);
+        seg_valid = c.ties != kAllTies;
+    }
+    kept.key = c.key;
+    kept.last = 0x7fffffff;
+    if (!seg_valid) return true;
+    // the index of the last kept token of that key: as many ties have a
+    // lower index as are kept before it
+    uint32_t* const ties = sm.hist.lo;  // and on into hi
+    constexpr int kRoom = 2 * kBuckets;
+    __syncthreads();
+    if (tid == 0) {
+        sm.last = 0x7fffffff;
+        sm.count = 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += NT) {
+        if (entry_key(list[i]) != c.key) continue;
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < kRoom) ties[at] = (uint32_t)entry_index(list[i]);
+    }
+    __syncthreads();
+    const int n_ties = sm.count;
+    if (n_ties > kRoom) return false;
+    for (int i = tid; i < n_ties; i += NT) {
+        u64 before = 0;
+        for (int j = 0; j < n_ties; ++j) before += ties[j] < ties[i] ? 1 : 0;
+        if (before + 1 == c.ties) sm.last = (int)ties[i];
+    }
+    __syncthreads();
+    kept.last = sm.last;
+    // the band's kept tokens join their segments
+    for (int i = tid; i < n; i += NT) {
+        const uint32_t k = entry_key(list[i]);
+        const int x = entry_index(list[i]);
+        if (k > kept.key || (k == kept.key && x <= kept.last))
+            atomicAdd(&sm.seg[(x + row.off) / (EPU * kSegU)], weight_of(key_value<DT>(k), sc, sm.table));
+    }
+    __syncthreads();
+    return true;
 }
 
 // The list that a row's kept set is taken from.
@@ -389,7 +566,7 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
                           List& l, TruncSmem<NT>& sm)
 {
     const int bm = xm > -INFINITY ? bucket_of(xm, sc.M) : kFar;
-    l.whole = row.V <= kListCap;
+    l.whole = row.V <= kWhole;
     if (st.T == 0.f) {
         l.top = 0;
     } else if (l.whole) {
@@ -399,11 +576,11 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
         l.top = bucket_of_kth<NT>(g, sc.M, st.k, sm.hist, sm.bs);
         if (st.p >= 1.f) l.top = min(l.top, bm);
     } else if (st.p < 1.f) {
-        l.top = bucket_of_share<NT>(g, st.p, sc, sm);
-        if (l.top == kFar) {
-            // the groups' largest tokens alone do not hold the share: as many
-            // tokens as a list has room for, if they are spread at random
-            // (n tokens then lie in G (1 - exp(-n / G)) of G groups)
+        bool near_miss;
+        l.top = bucket_of_share<NT>(g, st.p, sc, sm, near_miss);
+        if (l.top == kFar && near_miss) {
+            // as many tokens as a list has room for, if they are spread at
+            // random (n tokens then lie in G (1 - exp(-n / G)) of G groups)
             const int some = (int)((float)g.n * (1.f - __expf(-0.8f * kListCap / (float)g.n)));
             l.top = bucket_of_kth<NT>(g, sc.M, some, sm.hist, sm.bs);
         }
@@ -695,14 +872,18 @@ __device__ void write_row(const Row& row, void* out, const Kept& c, bool bad)
     }
 }
 
+// One CTA per row.  CTAs of 512 threads, two on an SM: 2048 rows of 151936
+// bf16 with top-k and top-p written 247 us, against 269 us with four CTAs of
+// 256 threads (top-p draws 166 us and 165 us).  Persistent CTAs that prefetch
+// their next row to L2 were slower (242 to 293 us with more prefetched): the
+// pass over the row is bound by instruction issue, not by HBM.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, int groups)
 {
     using E = Elem<DT>;
     __shared__ TruncSmem<NT> sm;
     extern __shared__ u64 list[];  // [kListCap], then the groups' maxima and sums
-    const int r = blockIdx.x;
-    const int tid = threadIdx.x;
+    const int r = blockIdx.x, tid = threadIdx.x;
     for (int i = tid; i < 64; i += NT) sm.table[i] = kExp2Table[i];
     Row row = row_at<DT>(a.logits, r, a.stride, a.V);
     stage_edges<DT>(row, sm.edge);
@@ -711,10 +892,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
     set_scale(sc, st.ok ? st.T : 0.f);
     if (tid == 0 && st.ok && st.m > 0.f)
         sm.min_p_off = min_p_offset(st.T, a.row_min_p ? log((double)st.m) : a.log_min_p);
-    float* const gmax = reinterpret_cast<float*>(list + kListCap);
-    const Groups g = groups_of<DT>(row, gmax, gmax + groups);
+    // a top_k near the number of lines is found among finer groups
+    const bool finer = st.k > 256 && st.k < a.V;
+    const Groups g = groups_of<DT>(row, reinterpret_cast<float*>(list + kListCap), groups, finer);
     // the row's whole mass matters where top_p is taken of it
-    const bool sums = st.T > 0.f && st.p < 1.f && !(st.k > 0 && st.k < a.V) && a.V > kListCap;
+    const bool sums = st.T > 0.f && st.p < 1.f && !(st.k > 0 && st.k < a.V) && a.V > kWhole;
     float m = sums ? scan_groups<DT, NT, true>(row, g, sc.ch) : scan_groups<DT, NT, false>(row, g, sc.ch);
     sc.M = block_max_nan<NT>(m, sm.bs);
     const bool finite = sc.M > -INFINITY && sc.M < INFINITY;
@@ -767,14 +949,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
             return;
         }
     }
-    c = find_kept<DT, NT>(row, st, sc, sm);
+    bool seg_valid = false;
+    if (!sums || !band_kept<DT, NT>(row, st, sc, xm, list, sm, c, seg_valid)) {
+        c = find_kept<DT, NT>(row, st, sc, sm);
+        seg_valid = false;
+    }
     if (out) write_row<DT, NT>(row, out, c, false);
     if (!tokens) return;
     const auto mass = [&](float x, int i) {
         return is_kept<DT>(x, i, c) ? (st.T > 0.f ? weight_of(x, sc, sm.table) : 1ull) : 0ull;
     };
     __syncthreads();
-    segment_sums<DT, NT>(row, sm.seg, mass);
+    if (!seg_valid) segment_sums<DT, NT>(row, sm.seg, mass);
     __syncthreads();
     u64 S = 0;
     for (int i = tid & 31; i < (row.n_units + kSegU - 1) / kSegU; i += 32) S += sm.seg[i];
@@ -785,9 +971,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
     }
 }
 
-template <int DT, int NT>
+template <int DT>
 cudaError_t launch(const TruncArgs& a, cudaStream_t st)
 {
+    constexpr int NT = 512;
     const int groups = groups_bound(a.V, Elem<DT>::kPerUnit);
     const size_t smem = kListCap * sizeof(u64) + (size_t)groups * 2 * sizeof(float);
     auto* kernel = truncate_kernel<DT, NT>;
@@ -801,8 +988,7 @@ cudaError_t launch(const TruncArgs& a, cudaStream_t st)
 
 cudaError_t launch_truncate(const TruncArgs& a, cudaStream_t st)
 {
-    if (a.n_rows <= 304) return a.dtype == SDV_F32 ? launch<SDV_F32, 512>(a, st) : launch<SDV_BF16, 512>(a, st);
-    return a.dtype == SDV_F32 ? launch<SDV_F32, 256>(a, st) : launch<SDV_BF16, 256>(a, st);
+    return a.dtype == SDV_F32 ? launch<SDV_F32>(a, st) : launch<SDV_BF16>(a, st);
 }
 
 }  // namespace sdv

@@ -104,6 +104,17 @@ def test_wide_kept_sets(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [3072, 3073, 8191, 50021, 151936])
+def test_flat_rows(dtype, V):
+    """Kept sets from a few hundred tokens to most of the row, where lists end and whole-row passes begin."""
+    for std, T, p in ((3.0, 1.0, 0.9), (2.0, 1.0, 0.9), (3.0, 1.2, 0.95), (2.0, 0.6, 0.8), (1.0, 1.0, 0.99)):
+        x = _rows(2, V, dtype, 33 + V, std=std)
+        _check(x, T, p=p, draws=5)
+        _check(x, T, p=p, m=0.01, draws=5)
+    _check(_rows(2, V, dtype, 34 + V, std=2.0)[:, 3:], 1.0, p=0.9, draws=5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [1000, 40007])
 def test_ties(dtype, V):
     """Few distinct values: borders inside ties go by index."""
