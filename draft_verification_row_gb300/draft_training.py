@@ -1,0 +1,118 @@
+"""A draft head trained on a target's rows, and verified as servers sample.
+
+Speculative decoding gains by the tokens of its drafts that verification
+accepts, and those by how near the draft model's distributions are to the
+target's ("Speculative Decoding: Performance or Illusion?", section 3.2).
+This module runs the library's operators around verification together, as a
+program that trains and serves a draft model would:
+
+  training    target rows -> top_logits (the teacher's records) ->
+              distill_loss on the draft head's rows -> its gradient -> a step
+              of the optimizer;
+  serving     draft rows -> sample_truncated (the drafted tokens, under
+              top-k, top-p and min-p) -> truncate_rows of both models' rows
+              -> block verification of the drafts.
+
+There are no trained weights here, so the target is a random linear map of
+random hidden states (bf16 rows, as an LM head writes them), and the draft a
+low-rank head of the same states.
+"""
+from dataclasses import dataclass
+
+import torch
+
+from . import binding
+
+
+@dataclass
+class Sampling:
+    """How tokens are drawn, by both models."""
+    temperature: float = 0.8
+    top_k: int = 50
+    top_p: float = 0.95
+    min_p: float = 0.0
+
+
+class DraftHead(torch.nn.Module):
+    """Logits of a hidden state through a bottleneck: rank * (d + V) weights."""
+
+    def __init__(self, d, V, rank, device, seed=0):
+        super().__init__()
+        g = torch.Generator(device=device).manual_seed(seed)
+        self.down = torch.nn.Parameter(torch.randn((d, rank), generator=g, device=device) / d ** 0.5)
+        self.up = torch.nn.Parameter(torch.randn((rank, V), generator=g, device=device) / rank ** 0.5)
+
+    def forward(self, hidden):
+        return ((hidden @ self.down) @ self.up).bfloat16()
+
+
+def target_rows(hidden, lm_head):
+    """The target's logits of each hidden state (bf16)."""
+    return (hidden @ lm_head).bfloat16()
+
+
+def train_step(head, optimizer, hidden, lm_head, *, k=32, temperature=1.0):
+    """One step on the rows of `hidden`; returns the mean loss (a tensor)."""
+    n = hidden.shape[0]
+    values, index, rest, _ = binding.top_logits(target_rows(hidden, lm_head), k, temperature)
+    weight = torch.full((n,), 1.0 / n, device=hidden.device)
+    loss = binding.distill_loss(head(hidden), values, index, rest, temperature=temperature, row_weight=weight).sum()
+    optimizer.zero_grad(set_to_none=True)
+    loss.backward()
+    optimizer.step()
+    return loss.detach()
+
+
+@torch.no_grad()
+def verify_drafts(head, hidden, lm_head, sampling, seed=0):
+    """Draft and verify a batch: hidden [B][L+1][d], one draft of L tokens per
+    request.  Returns verify's outputs (accept_len among them) and the status
+    bits of every call."""
+    B, Lp1, d = hidden.shape
+    L, V, dev = Lp1 - 1, lm_head.shape[1], hidden.device
+    g = torch.Generator(device=dev).manual_seed(seed)
+    cut = dict(top_k=sampling.top_k, top_p=sampling.top_p, min_p=sampling.min_p)
+    target = target_rows(hidden.reshape(-1, d), lm_head)
+    draft = head(hidden[:, :L].reshape(-1, d))
+    u = torch.rand((B * L, 1), generator=g, device=dev)
+    tokens, s1 = binding.sample_truncated(draft, 1, u, sampling.temperature, **cut)
+    target, s2 = binding.truncate_rows(target, sampling.temperature, **cut, out=target)
+    draft, s3 = binding.truncate_rows(draft, sampling.temperature, **cut, out=draft)
+    out = binding.verify("block", target.view(B, 1, Lp1, V), draft.view(B, 1, L, V), tokens.view(B, 1, L), None,
+                         torch.rand((B, 1, L), generator=g, device=dev),
+                         torch.rand((B, 1, Lp1), generator=g, device=dev), sampling.temperature)
+    return out, s1 | s2 | s3 | out["device_status"]
+
+
+def run(steps=200, rows=2048, B=256, L=4, V=32000, d=128, rank=64, lr=2e-2, device="cuda:0", sampling=None, seed=0):
+    """Train a draft head for some steps; returns its losses and the mean
+    accepted length before and after."""
+    sampling = sampling or Sampling()
+    dev = torch.device(device)
+    g = torch.Generator(device=dev).manual_seed(seed)
+    lm_head = torch.randn((d, V), generator=g, device=dev) * (2.5 / d ** 0.5)
+    # hidden states near a subspace that the bottleneck can hold
+    basis = torch.randn((rank // 2, d), generator=g, device=dev)
+
+    def states(*shape):
+        x = torch.randn((*shape, rank // 2), generator=g, device=dev) @ basis
+        return x / (rank // 2) ** 0.5 + 0.1 * torch.randn((*shape, d), generator=g, device=dev)
+
+    head = DraftHead(d, V, rank, dev, seed)
+    optimizer = torch.optim.Adam(head.parameters(), lr=lr)
+    held_out = states(B, L + 1)
+    before, s0 = verify_drafts(head, held_out, lm_head, sampling)
+    losses = [train_step(head, optimizer, states(rows), lm_head) for _ in range(steps)]
+    after, s1 = verify_drafts(head, held_out, lm_head, sampling)
+    status = int((s0 | s1).item())
+    if status:
+        raise RuntimeError(f"device status {status}")
+    return {"losses": torch.stack(losses).tolist(),
+            "accepted_before": before["accept_len"].float().mean().item(),
+            "accepted_after": after["accept_len"].float().mean().item()}
+
+
+if __name__ == "__main__":
+    r = run()
+    print(f"loss {r['losses'][0]:.3f} -> {r['losses'][-1]:.3f}; accepted draft tokens per request "
+          f"{r['accepted_before']:.2f} -> {r['accepted_after']:.2f} of 4")
