@@ -293,13 +293,18 @@ def sample_rows(logits, n_samples, u, temperature, *, V=None, tokens=None, devic
 
 def _rows(name, t, V):
     """(n_rows, V, row stride) of a CUDA [n_rows][width] tensor with contiguous rows."""
-    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+    if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a CUDA [n_rows][width] tensor with contiguous rows")
     n, width = t.shape
-    V = width if V is None else int(V)
-    if V > width:
+    stride, step = t.stride()
+    if step != 1 and width > 1:
+        raise ValueError(f"{name} must be a CUDA [n_rows][width] tensor with contiguous rows")
+    if V is None:
+        V = width
+    elif V > width:
         raise ValueError(f"{name} has fewer than V = {V} columns")
-    stride = t.stride(0) if n > 1 else width
+    if n <= 1:
+        stride = width
     if stride < V:
         raise ValueError(f"{name}'s rows overlap")
     return n, V, stride
@@ -307,7 +312,7 @@ def _rows(name, t, V):
 
 def _vector(name, t, n, dtype, device):
     """A contiguous [n] array on the rows' device, or None."""
-    if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous() or tuple(t.shape) != (n,)):
+    if t is not None and (t.dtype != dtype or t.device != device or not t.is_contiguous() or t.shape != (n,)):
         raise ValueError(f"{name} must be a contiguous {dtype} [n_rows] tensor on the rows' device")
     return t
 
@@ -337,9 +342,18 @@ def _settings(n, device, temperature, top_k, top_p, min_p):
     return common, arrays
 
 
-def _status(device_status, device):
+def _empty(shape, dtype, device, stream):
+    """A new output; where the call runs on a stream of its own, its memory is not given away before that stream has
+    passed it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _status(device_status, device, stream):
     if device_status is None:
-        return torch.empty(1, dtype=torch.int32, device=device)
+        return _empty(1, torch.int32, device, stream)
     return _vector("device_status", device_status, 1, torch.int32, device)
 
 
@@ -366,15 +380,15 @@ def sample_truncated(logits, n_samples, u, temperature, *, top_k=0, top_p=1.0, m
     if n_samples < 1:
         raise ValueError("n_samples must be at least 1")
     if u is not None and (u.dtype != torch.float32 or u.device != logits.device or not u.is_contiguous()
-                          or tuple(u.shape) != (n, n_samples)):
+                          or u.shape != (n, n_samples)):
         raise ValueError("u must be a contiguous CUDA float32 [n_rows][n_samples] tensor")
     common, arrays = _settings(n, logits.device, temperature, top_k, top_p, min_p)
     if tokens is None:
-        tokens = torch.empty((n, n_samples), dtype=torch.int32, device=logits.device)
+        tokens = _empty((n, n_samples), torch.int32, logits.device, stream)
     elif (tokens.dtype != torch.int32 or tokens.device != logits.device or not tokens.is_contiguous()
-          or tuple(tokens.shape) != (n, n_samples)):
+          or tokens.shape != (n, n_samples)):
         raise ValueError("tokens must be a contiguous CUDA int32 [n_rows][n_samples] tensor")
-    device_status = _status(device_status, logits.device)
+    device_status = _status(device_status, logits.device, stream)
     rc = h.sdv_sample_truncated(n, V, stride, _dtype_code(logits), *common, *map(_addr, arrays), _addr(logits), n_samples,
                                 _addr(u), _addr(tokens), _addr(device_status), _stream(stream, logits.device))
     if rc != 0:
@@ -395,11 +409,11 @@ def truncate_rows(logits, temperature, *, top_k=0, top_p=1.0, min_p=0.0, V=None,
     n, V, stride = _rows("logits", logits, V)
     common, arrays = _settings(n, logits.device, temperature, top_k, top_p, min_p)
     if out is None:
-        out = torch.empty((n, V), dtype=logits.dtype, device=logits.device)
+        out = _empty((n, V), logits.dtype, logits.device, stream)
     n_out, _, out_stride = _rows("out", out, V)
     if n_out != n or out.dtype != logits.dtype or out.device != logits.device:
         raise ValueError("out must have the logits' rows, type and device")
-    device_status = _status(device_status, logits.device)
+    device_status = _status(device_status, logits.device, stream)
     rc = h.sdv_truncate_rows(n, V, stride, _dtype_code(logits), *common, *map(_addr, arrays), _addr(logits), _addr(out),
                              out_stride, _addr(device_status), _stream(stream, logits.device))
     if rc != 0:
@@ -419,10 +433,10 @@ def top_logits(logits, k, temperature=1.0, *, V=None, device_status=None, stream
     k, dev = _c_int("k", k), logits.device
     if k < 1:
         raise ValueError("k must be at least 1")
-    values = torch.empty((n, k), dtype=logits.dtype, device=dev)
-    index = torch.empty((n, k), dtype=torch.int32, device=dev)
-    rest = torch.empty(n, dtype=torch.float32, device=dev)
-    device_status = _status(device_status, dev)
+    values = _empty((n, k), logits.dtype, dev, stream)
+    index = _empty((n, k), torch.int32, dev, stream)
+    rest = _empty(n, torch.float32, dev, stream)
+    device_status = _status(device_status, dev, stream)
     rc = h.sdv_top_logits(n, V, stride, _dtype_code(logits), float(temperature), _addr(logits), k, _addr(values),
                           _addr(index), _addr(rest), _addr(device_status), _stream(stream, dev))
     if rc != 0:
@@ -448,11 +462,11 @@ def distill_forward(student, values, index, rest=None, *, temperature=1.0, row_w
     distill_backward, or None.  Returns (loss [n_rows] float32, device_status)."""
     h = lib()
     n, V, stride = _record(student, values, index, rest, row_weight, V)
-    loss = torch.empty(n, dtype=torch.float32, device=student.device)
+    loss = _empty(n, torch.float32, student.device, stream)
     if stats is not None and (stats.dtype != torch.float32 or tuple(stats.shape) != (n, 4)
                               or not stats.is_contiguous() or stats.device != student.device):
         raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
-    device_status = _status(device_status, student.device)
+    device_status = _status(device_status, student.device, stream)
     rc = h.sdv_distill_forward(n, V, stride, _dtype_code(student), float(temperature), _addr(student), values.shape[1],
                                _dtype_code(values), _addr(values), _addr(index), _addr(rest), _addr(row_weight),
                                _addr(loss), _addr(stats), _addr(device_status), _stream(stream, student.device))
@@ -461,11 +475,12 @@ def distill_forward(student, values, index, rest=None, *, temperature=1.0, row_w
     return loss, device_status
 
 
-def _grad_rows(student, grad, n, V):
+def _grad_rows(student, grad, n, V, stream):
     if grad is None:
-        # columns past V, where there are any, have no gradient
-        shape = student.shape
-        grad = (torch.empty if V == shape[1] else torch.zeros)(shape, dtype=student.dtype, device=student.device)
+        grad = _empty(student.shape, student.dtype, student.device, stream)
+        if V < student.shape[1]:  # columns past V have no gradient
+            with torch.cuda.stream(stream):
+                grad[:, V:].zero_()
     n_grad, _, stride = _rows("grad", grad, V)
     if n_grad != n or grad.dtype != student.dtype or grad.device != student.device:
         raise ValueError("grad must have the student's rows, type and device")
@@ -482,7 +497,7 @@ def distill_backward(student, values, index, rest, stats, grad_loss=None, *, tem
             or stats.device != student.device):
         raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
     _vector("grad_loss", grad_loss, n, torch.float32, student.device)
-    grad, grad_stride = _grad_rows(student, grad, n, V)
+    grad, grad_stride = _grad_rows(student, grad, n, V, stream)
     rc = h.sdv_distill_backward(n, V, stride, _dtype_code(student), float(temperature), _addr(student), values.shape[1],
                                 _dtype_code(values), _addr(values), _addr(index), _addr(rest), _addr(row_weight),
                                 _addr(stats), _addr(grad_loss), _addr(grad), grad_stride,
@@ -499,9 +514,9 @@ def distill_loss_grad(student, values, index, rest=None, *, temperature=1.0, row
     student's type, device_status)."""
     h = lib()
     n, V, stride = _record(student, values, index, rest, row_weight, V)
-    loss = torch.empty(n, dtype=torch.float32, device=student.device)
-    grad, grad_stride = _grad_rows(student, grad, n, V)
-    device_status = _status(device_status, student.device)
+    loss = _empty(n, torch.float32, student.device, stream)
+    grad, grad_stride = _grad_rows(student, grad, n, V, stream)
+    device_status = _status(device_status, student.device, stream)
     rc = h.sdv_distill_loss_grad(n, V, stride, _dtype_code(student), float(temperature), _addr(student),
                                  values.shape[1], _dtype_code(values), _addr(values), _addr(index), _addr(rest),
                                  _addr(row_weight), _addr(loss), _addr(grad), grad_stride, _addr(device_status),
@@ -514,11 +529,9 @@ def distill_loss_grad(student, values, index, rest=None, *, temperature=1.0, row
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, student, values, index, rest, row_weight, temperature, V):
-        stats = None
-        if ctx.needs_input_grad[0]:
-            stats = torch.empty((student.shape[0], 4), dtype=torch.float32, device=student.device)
-            ctx.save_for_backward(student, values, index, rest, row_weight, stats)
-            ctx.settings = dict(temperature=temperature, V=V)
+        stats = torch.empty((student.shape[0], 4), dtype=torch.float32, device=student.device)
+        ctx.save_for_backward(student, values, index, rest, row_weight, stats)
+        ctx.settings = dict(temperature=temperature, V=V)
         return distill_forward(student, values, index, rest, temperature=temperature, row_weight=row_weight, V=V,
                                stats=stats)[0]
 
@@ -541,6 +554,8 @@ def distill_loss(student, values, index, rest=None, *, temperature=1.0, row_weig
     row_weight * KL(teacher || student) over the record's tokens and one outcome for all others, at temperature T.
     The teacher's record and the weights get no gradient.
     """
+    if not (student.requires_grad and torch.is_grad_enabled()):
+        return distill_forward(student, values, index, rest, temperature=temperature, row_weight=row_weight, V=V)[0]
     return _DistillLoss.apply(student, values, index, rest, row_weight, float(temperature), V)
 
 
