@@ -112,7 +112,8 @@ def lib(path: str = LIB_PATH):
     h.sdv_distill_forward.restype = ctypes.c_int
     h.sdv_distill_forward.argtypes = rows + record + [ctypes.c_void_p] * 4
     h.sdv_distill_backward.restype = ctypes.c_int
-    h.sdv_distill_backward.argtypes = rows + record + [ctypes.c_void_p] * 3 + [ctypes.c_longlong, ctypes.c_void_p]
+    h.sdv_distill_backward.argtypes = (rows + record + [ctypes.c_void_p] * 2 + [ctypes.c_longlong, ctypes.c_void_p,
+                                                                                ctypes.c_longlong, ctypes.c_void_p])
     h.sdv_distill_loss_grad.restype = ctypes.c_int
     h.sdv_distill_loss_grad.argtypes = (rows + record + [ctypes.c_void_p] * 2 + [ctypes.c_longlong]
                                         + [ctypes.c_void_p] * 2)
@@ -456,23 +457,34 @@ def _record(student, values, index, rest, row_weight, V):
     return n, V, stride
 
 
+def _stats_ok(stats, n, device):
+    if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous() or stats.device != device:
+        raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
+
+
+def _forward(sizes, student, values, index, rest, temperature, row_weight, stats, device_status, stream):
+    """sdv_distill_forward on checked arguments (sizes: n_rows, V, row stride)."""
+    loss = _empty(sizes[0], torch.float32, student.device, stream)
+    rc = _lib.sdv_distill_forward(*sizes, _dtype_code(student), temperature, student.data_ptr(), values.shape[1],
+                                  _dtype_code(values), values.data_ptr(), index.data_ptr(), _addr(rest),
+                                  _addr(row_weight), loss.data_ptr(), _addr(stats), _addr(device_status),
+                                  _stream(stream, student.device))
+    if rc != 0:
+        raise SDVError(rc, "sdv_distill_forward")
+    return loss
+
+
 def distill_forward(student, values, index, rest=None, *, temperature=1.0, row_weight=None, V=None, stats=None,
                     device_status=None, stream=None):
     """The distillation loss of each row (sdv_distill_forward); stats: a [n_rows][4] float32 tensor to be written for
     distill_backward, or None.  Returns (loss [n_rows] float32, device_status)."""
-    h = lib()
-    n, V, stride = _record(student, values, index, rest, row_weight, V)
-    loss = _empty(n, torch.float32, student.device, stream)
-    if stats is not None and (stats.dtype != torch.float32 or tuple(stats.shape) != (n, 4)
-                              or not stats.is_contiguous() or stats.device != student.device):
-        raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
+    lib()
+    sizes = _record(student, values, index, rest, row_weight, V)
+    if stats is not None:
+        _stats_ok(stats, sizes[0], student.device)
     device_status = _status(device_status, student.device, stream)
-    rc = h.sdv_distill_forward(n, V, stride, _dtype_code(student), float(temperature), _addr(student), values.shape[1],
-                               _dtype_code(values), _addr(values), _addr(index), _addr(rest), _addr(row_weight),
-                               _addr(loss), _addr(stats), _addr(device_status), _stream(stream, student.device))
-    if rc != 0:
-        raise SDVError(rc, "sdv_distill_forward")
-    return loss, device_status
+    return _forward(sizes, student, values, index, rest, float(temperature), row_weight, stats, device_status,
+                    stream), device_status
 
 
 def _grad_rows(student, grad, n, V, stream):
@@ -493,14 +505,12 @@ def distill_backward(student, values, index, rest, stats, grad_loss=None, *, tem
     distill_forward's inputs and stats.  Returns grad, of the student's type."""
     h = lib()
     n, V, stride = _record(student, values, index, rest, row_weight, V)
-    if (stats.dtype != torch.float32 or tuple(stats.shape) != (n, 4) or not stats.is_contiguous()
-            or stats.device != student.device):
-        raise ValueError("stats must be a contiguous CUDA float32 [n_rows][4] tensor")
+    _stats_ok(stats, n, student.device)
     _vector("grad_loss", grad_loss, n, torch.float32, student.device)
     grad, grad_stride = _grad_rows(student, grad, n, V, stream)
     rc = h.sdv_distill_backward(n, V, stride, _dtype_code(student), float(temperature), _addr(student), values.shape[1],
                                 _dtype_code(values), _addr(values), _addr(index), _addr(rest), _addr(row_weight),
-                                _addr(stats), _addr(grad_loss), _addr(grad), grad_stride,
+                                _addr(stats), _addr(grad_loss), 1, _addr(grad), grad_stride,
                                 _stream(stream, student.device))
     if rc != 0:
         raise SDVError(rc, "sdv_distill_backward")
@@ -528,20 +538,28 @@ def distill_loss_grad(student, values, index, rest=None, *, temperature=1.0, row
 
 class _DistillLoss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, student, values, index, rest, row_weight, temperature, V):
-        stats = torch.empty((student.shape[0], 4), dtype=torch.float32, device=student.device)
+    def forward(ctx, student, values, index, rest, row_weight, temperature, sizes):
+        stats = torch.empty((sizes[0], 4), dtype=torch.float32, device=student.device)
         ctx.save_for_backward(student, values, index, rest, row_weight, stats)
-        ctx.settings = dict(temperature=temperature, V=V)
-        return distill_forward(student, values, index, rest, temperature=temperature, row_weight=row_weight, V=V,
-                               stats=stats)[0]
+        ctx.temperature, ctx.sizes = temperature, sizes
+        return _forward(sizes, student, values, index, rest, temperature, row_weight, stats, None, None)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss):
+        if torch.is_grad_enabled():  # create_graph
+            raise RuntimeError("the gradient of distill_loss cannot be differentiated again")
         student, values, index, rest, row_weight, stats = ctx.saved_tensors
-        grad = distill_backward(student, values, index, rest, stats, grad_loss.float().contiguous(),
-                                row_weight=row_weight, **ctx.settings)
-        return (grad,) + (None,) * 6
+        n, V, _ = ctx.sizes
+        grad, grad_stride = _grad_rows(student, None, n, V, None)
+        # a sum's upstream gradient is one number for all rows (stride 0)
+        rc = _lib.sdv_distill_backward(*ctx.sizes, _dtype_code(student), ctx.temperature, student.data_ptr(),
+                                       values.shape[1], _dtype_code(values), values.data_ptr(), index.data_ptr(),
+                                       _addr(rest), _addr(row_weight), stats.data_ptr(), grad_loss.data_ptr(),
+                                       grad_loss.stride(0), grad.data_ptr(), grad_stride,
+                                       _stream(None, student.device))
+        if rc != 0:
+            raise SDVError(rc, "sdv_distill_backward")
+        return grad, None, None, None, None, None, None
 
 
 def distill_loss(student, values, index, rest=None, *, temperature=1.0, row_weight=None, V=None):
@@ -554,9 +572,11 @@ def distill_loss(student, values, index, rest=None, *, temperature=1.0, row_weig
     row_weight * KL(teacher || student) over the record's tokens and one outcome for all others, at temperature T.
     The teacher's record and the weights get no gradient.
     """
+    lib()
+    sizes = _record(student, values, index, rest, row_weight, V)
     if not (student.requires_grad and torch.is_grad_enabled()):
-        return distill_forward(student, values, index, rest, temperature=temperature, row_weight=row_weight, V=V)[0]
-    return _DistillLoss.apply(student, values, index, rest, row_weight, float(temperature), V)
+        return _forward(sizes, student, values, index, rest, float(temperature), row_weight, None, None, None)
+    return _DistillLoss.apply(student, values, index, rest, row_weight, float(temperature), sizes)
 
 
 def _bf16_rows(name, t, d=None):

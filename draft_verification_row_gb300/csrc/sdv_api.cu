@@ -756,13 +756,15 @@ int sdv_distill_forward(int n_rows, int V, long long row_stride, int dtype, floa
 
 int sdv_distill_backward(int n_rows, int V, long long row_stride, int dtype, float temperature, const void* student,
                          int k, int teacher_dtype, const void* values, const int* index, const float* rest,
-                         const float* row_weight, const float* stats, const float* grad_loss, void* grad,
-                         long long grad_stride, void* cuda_stream)
+                         const float* row_weight, const float* stats, const float* grad_loss,
+                         long long grad_loss_stride, void* grad, long long grad_stride, void* cuda_stream)
 {
+    if (grad_loss && (grad_loss_stride < 0 || grad_loss_stride > (1ll << 40))) return SDV_ERR_INVALID;
     sdv::DistillArgs a = distill_args(n_rows, V, row_stride, dtype, student, k, teacher_dtype, values, index, rest,
                                       row_weight);
     a.stats = const_cast<float*>(stats);
     a.grad_loss = grad_loss;
+    a.grad_loss_stride = grad_loss_stride;
     a.grad = grad;
     a.grad_stride = grad_stride;
     return distill(a, temperature, false, true, cuda_stream);

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
         fill_row<DT, NT>(grow, 0.f);
         return;
     }
-    const float scale = weight * (a.grad_loss ? a.grad_loss[r] : 1.f) * a.inv_T;
+    const float scale = weight * (a.grad_loss ? a.grad_loss[r * a.grad_loss_stride] : 1.f) * a.inv_T;
     // another token: scale (q_i - p_r q_i / q_r), both against mo, so that
     // neither factor is lost where the k tokens hold nearly all of the mass
     const float fo = mo > -INFINITY ? scale * (ex2((mo - M) * a.c) / Z - pr / zo) : 0.f;

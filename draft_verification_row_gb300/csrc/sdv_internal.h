@@ -144,7 +144,8 @@ struct DistillArgs {
     const int* index;        // [n_rows][k]
     const float* rest;       // [n_rows] or NULL
     const float* row_weight; // [n_rows] or NULL
-    const float* grad_loss;  // [n_rows] or NULL (1)
+    const float* grad_loss;  // or NULL (1)
+    long long grad_loss_stride;
     float* loss;             // [n_rows]; NULL: backward (stats are read)
     float* stats;            // [n_rows][4]: {mo, zo, M, Z}; forward: written, or NULL
     void* grad;              // [n_rows][grad_stride]; NULL: forward

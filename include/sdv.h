@@ -342,8 +342,9 @@ int sdv_top_logits(int n_rows, int V, long long row_stride, int dtype, float tem
  *                its loss and gradient are NaN (SDV_REQ_NONFINITE).
  *   stats        [n_rows][4] fp32, written by sdv_distill_forward (or NULL)
  *                for sdv_distill_backward on the same inputs.
- *   grad_loss    [n_rows] fp32 or NULL (1): the derivative of what is
- *                minimised with respect to each row's loss.
+ *   grad_loss    fp32 or NULL (1): the derivative of what is minimised with
+ *                respect to each row's loss, grad_loss_stride elements
+ *                apart (>= 0; 0: one number for all rows).
  *   grad         [n_rows][grad_stride] of dtype, out; grad_stride >= V.  May
  *                be student itself with the same stride (in place);
  *                otherwise the two must not overlap.
@@ -356,8 +357,8 @@ int sdv_distill_forward(int n_rows, int V, long long row_stride, int dtype, floa
                         const float *row_weight, float *loss, float *stats, int *device_status, void *cuda_stream);
 int sdv_distill_backward(int n_rows, int V, long long row_stride, int dtype, float temperature, const void *student,
                          int k, int teacher_dtype, const void *values, const int *index, const float *rest,
-                         const float *row_weight, const float *stats, const float *grad_loss, void *grad,
-                         long long grad_stride, void *cuda_stream);
+                         const float *row_weight, const float *stats, const float *grad_loss,
+                         long long grad_loss_stride, void *grad, long long grad_stride, void *cuda_stream);
 int sdv_distill_loss_grad(int n_rows, int V, long long row_stride, int dtype, float temperature, const void *student,
                           int k, int teacher_dtype, const void *values, const int *index, const float *rest,
                           const float *row_weight, float *loss, void *grad, long long grad_stride,

@@ -273,6 +273,11 @@ def test_autograd(dtype):
     half = torch.finfo(DT[dtype]).eps / 2
     assert ((student.grad - want).float().abs() <= want.float().abs() * (2 * half + TOL) + 1e-7).all()
     assert not sdv.distill_loss(student.detach(), values, index, rest, V=3001).requires_grad
+    with torch.no_grad():
+        assert not sdv.distill_loss(student, values, index, rest, V=3001).requires_grad
+    loss = sdv.distill_loss(student, values, index, rest, V=3001).sum()
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        torch.autograd.grad(loss, student, create_graph=True)
 
 
 def test_in_place_repeat_and_graph():

@@ -61,7 +61,7 @@ def test_top_and_distill_refusals(lib, over):
     head = (a["n"], a["V"], a["stride"], a["dtype"], a["T"], None, a["k"])
     assert lib.sdv_top_logits(*head, None, None, None, None, None) == 1
     assert lib.sdv_distill_forward(*head, 0, None, None, None, None, None, None, None, None) == 1
-    assert lib.sdv_distill_backward(*head, 0, None, None, None, None, None, None, None, a["V"], None) == 1
+    assert lib.sdv_distill_backward(*head, 0, None, None, None, None, None, None, 1, None, a["V"], None) == 1
     assert lib.sdv_distill_loss_grad(*head, 0, None, None, None, None, None, None, a["V"], None, None) == 1
 
 
