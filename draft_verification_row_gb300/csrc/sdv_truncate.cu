@@ -30,14 +30,16 @@ namespace sdv {
 namespace {
 
 constexpr int kMaxSeg = (SDV_MAX_V / 4 + 1 + kSegU - 1) / kSegU;  // segments of the longest row
-constexpr int kListCap = 8192;                                    // listed tokens
-constexpr int kWhole = 3072;                                      // rows up to this length are listed whole
+constexpr int kWhole = 2048;                                      // rows up to this length are listed whole
 
-constexpr int kShort = 256;  // lists up to this length are ranked by counting
+// Listed tokens.
+template <int NT>
+constexpr int kListCap = NT == 512 ? 8192 : 2048;
 
-struct Band {  // buckets
-    int lo, hi;
-};
+
+// Lists up to this length are ranked by counting.
+template <int NT>
+constexpr int kShort = 256;
 
 template <int NT>
 struct TruncSmem {
@@ -47,7 +49,7 @@ struct TruncSmem {
     u64 seg[kMaxSeg];  // per segment: tied tokens, then kept mass
     int last;          // index of the last kept token of the border's key
     int count;         // band_kept: the band's tokens
-    Band band;
+    int2 band;
     float2 min_p_off;  // T ln(min_p)
     uint4 edge[2];
 };
@@ -383,51 +385,59 @@ __device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncS
 // ------------------------------------------------------------------------
 // top_p of rows whose kept set no list can hold
 
-// What the row's tokens weigh by buckets, in fp32 up to 2^-13: a count of
-// 2^-13 shares of the bucket's largest weight, which 32 bits hold for any
-// row.  Then the buckets in which the share p of the row's mass may be
-// reached, as far as these sums can tell.
-__device__ __forceinline__ float bucket_exponent(int b, float c)
-{
-    // the least distance in bucket b, as an exponent, rounded down
-    const float t = b == 0 ? 0.f : __uint_as_float((uint32_t)(b + ((127 - 13) << 5)) << 18);
-    return floorf(t * c);
-}
+// Buckets by the exponent y of a token's weight 2^-y, 128 to an octave: 0 is
+// y < 1/4, the last one y >= 2^6, whose weights are nothing.
+constexpr int kBandShift = 16, kBandBase = (127 - 2) << 7;
 
+struct Band {
+    float M, ch;
+    __device__ __forceinline__ float y(float x) const { return (M - x) * ch; }
+    __device__ __forceinline__ int bucket(float x) const
+    {
+        return min(max((int)(__float_as_uint(y(x)) >> kBandShift) - kBandBase, 0), kFar);
+    }
+    // the least y of bucket b as a whole number: its weights are 2^-e to 2^-e / 4
+    static __device__ __forceinline__ float exponent(int b)
+    {
+        return b == 0 ? 0.f : floorf(__uint_as_float((uint32_t)(b + kBandBase) << kBandShift));
+    }
+};
+
+// The buckets in which the share p of the row's mass may be reached, from
+// what the row's tokens weigh by buckets: a count of 2^-13 shares of the
+// bucket's 2^-e, which 32 bits hold for any row and which is right to about
+// 2^-13 of each bucket's sum.  lo > hi: unknown.
 template <int DT, int NT>
-__device__ Band band_of_share(const Row& row, float p, const Scale& sc, TruncSmem<NT>& sm)
+__device__ int2 band_of_share(const Row& row, float p, const Scale& sc, TruncSmem<NT>& sm)
 {
     constexpr int kPer = kBuckets / NT;
     constexpr float kUnit = 8192.f;
     const int tid = threadIdx.x;
+    const Band by{sc.M, sc.ch};
     __syncthreads();
     for (int i = tid; i < kBuckets; i += NT) sm.hist.lo[i] = 0u;
-    if (tid == 0) sm.band = {kFar, -1};
+    if (tid == 0) sm.band = make_int2(kFar, -1);
     __syncthreads();
     const RowSource<DT, NT> src{row};
     src.each([&](float x) {
-        const float d = x - sc.M;
-        if (!(d * sc.ch >= -60.f)) return;  // 2^18 of these are nothing
-        const int b = bucket_of(x, sc.M);
-        atomicAdd(&sm.hist.lo[b], __float2uint_rn(ex2(fmaf(d, sc.ch, bucket_exponent(b, sc.ch))) * kUnit));
+        const int b = by.bucket(x);
+        if (b < kFar) atomicAdd(&sm.hist.lo[b], __float2uint_rn(ex2(Band::exponent(b) - by.y(x)) * kUnit));
     });
     __syncthreads();
     u64 v[kPer], sum = 0, total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int b = tid * kPer + i;
-        const float n = (float)sm.hist.lo[b];
-        v[i] = n > 0.f ? (u64)(n * ex2(-bucket_exponent(b, sc.ch)) * (kOne / kUnit)) : 0;
+        v[i] = (u64)((float)sm.hist.lo[b] * ex2(-Band::exponent(b)) * (kOne / kUnit));
         sum += v[i];
     }
-    const u64 before = block_scan<NT>(sum, total, sm.bs);
+    u64 run = block_scan<NT>(sum, total, sm.bs);
     const float share = p * (float)total;
     const u64 lo = (u64)(share * (1.f - 4e-4f)), hi = (u64)(share * (1.f + 4e-4f)) + 1;
-    u64 run = before;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        if (run <= lo && run + v[i] > lo) sm.band.lo = tid * kPer + i;
-        if (run < hi && run + v[i] >= hi) sm.band.hi = tid * kPer + i;
+        if (run <= lo && run + v[i] > lo) sm.band.x = tid * kPer + i;
+        if (run < hi && run + v[i] >= hi) sm.band.y = tid * kPer + i;
         run += v[i];
     }
     __syncthreads();
@@ -437,18 +447,19 @@ __device__ Band band_of_share(const Row& row, float p, const Scale& sc, TruncSme
 // The kept set of such a row: one pass in fixed point takes the mass above
 // the band by segments (seg), the band's tokens into the list, in any order,
 // and the rest's mass; the border is then searched in the list.  False: it
-// is not in the band, or the band is too long.  seg holds the kept mass of
+// is not in the band, or the band is longer than room (the list, and the
+// groups behind it, which are not needed any more).  seg holds the kept mass of
 // the row's segments afterwards, unless min_p ends the kept set earlier
 // (seg_valid).
 template <int DT, int NT>
-__device__ bool band_kept(const Row& row, const Settings& st, const Scale& sc, float xm, u64* list, TruncSmem<NT>& sm,
-                          Kept& kept, bool& seg_valid)
+__device__ bool band_kept(const Row& row, const Settings& st, const Scale& sc, float xm, u64* list, int room,
+                          TruncSmem<NT>& sm, Kept& kept, bool& seg_valid)
 {
     constexpr int EPU = Elem<DT>::kPerUnit;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const Band band = band_of_share<DT, NT>(row, st.p, sc, sm);
-    if (band.lo > band.hi || band.hi >= kFar) return false;
-    const Near above(sc.M, band.lo - 1), within(sc.M, band.hi);
+    const int2 band = band_of_share<DT, NT>(row, st.p, sc, sm);
+    if (band.x > band.y) return false;
+    const Band by{sc.M, sc.ch};
     if (tid == 0) sm.count = 0;
     __syncthreads();
     const int n_seg = (row.n_units + kSegU - 1) / kSegU;
@@ -461,13 +472,14 @@ __device__ bool band_kept(const Row& row, const Settings& st, const Scale& sc, f
 #pragma unroll
             for (int e = 0; e < EPU; ++e) {
                 const u64 wt = weight_of(v[e], sc, sm.table);
-                if (band.lo > 0 && above(v[e]))
+                const int b = by.bucket(v[e]);
+                if (b < band.x)
                     mine += wt;
-                else if (!within(v[e]))
+                else if (b > band.y)
                     low += wt;
                 else {
                     const int at = atomicAdd(&sm.count, 1);
-                    if (at < kListCap) list[at] = list_entry(key_of<DT>(v[e]), u * EPU + e - row.off);
+                    if (at < room) list[at] = list_entry(key_of<DT>(v[e]), u * EPU + e - row.off);
                 }
             }
         }
@@ -480,7 +492,7 @@ __device__ bool band_kept(const Row& row, const Settings& st, const Scale& sc, f
     high = block_sum<NT>(high, sm.bs);
     low = block_sum<NT>(low, sm.bs);
     const int n = sm.count;
-    if (n > kListCap || n == 0) return false;
+    if (n > room || n == 0) return false;
     const ListSource<DT, NT> src{list, n};
     u64 mid = 0;
     src.each([&](float x) { mid += weight_of(x, sc, sm.table); });
@@ -572,7 +584,7 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
     } else if (l.whole) {
         l.top = kFar;
     } else if (st.k > 0 && st.k < row.V) {
-        if (st.k > kListCap) return false;
+        if (st.k > kListCap<NT>) return false;
         l.top = bucket_of_kth<NT>(g, sc.M, st.k, sm.hist, sm.bs);
         if (st.p >= 1.f) l.top = min(l.top, bm);
     } else if (st.p < 1.f) {
@@ -581,7 +593,7 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
         if (l.top == kFar && near_miss) {
             // as many tokens as a list has room for, if they are spread at
             // random (n tokens then lie in G (1 - exp(-n / G)) of G groups)
-            const int some = (int)((float)g.n * (1.f - __expf(-0.8f * kListCap / (float)g.n)));
+            const int some = (int)((float)g.n * (1.f - __expf(-0.8f * kListCap<NT> / (float)g.n)));
             l.top = bucket_of_kth<NT>(g, sc.M, some, sm.hist, sm.bs);
         }
         l.top = min(l.top, bm);
@@ -591,12 +603,12 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
     l.ends = l.top == bm;
     if (l.top >= kFar && !l.whole) return false;
     float rest = 0.f;
-    l.n = collect<DT, NT>(row, g, Near(sc.M, l.top), l.at, kListCap, l.low, sm.hist, sm.bs,
+    l.n = collect<DT, NT>(row, g, Near(sc.M, l.top), l.at, kListCap<NT>, l.low, sm.hist, sm.bs,
                           [&](const uint4& raw, uint32_t marks) {
                               if (sums) rest += unit_sum<DT>(without<DT>(raw, marks), sc.ch, sc.M);
                           });
     l.rest = rest;
-    return l.n <= kListCap;
+    return l.n <= kListCap<NT>;
 }
 
 // The mass of what is not listed, in fp32 sums (bucket_of_share has taken the
@@ -872,17 +884,13 @@ __device__ void write_row(const Row& row, void* out, const Kept& c, bool bad)
     }
 }
 
-// One CTA per row.  CTAs of 512 threads, two on an SM: 2048 rows of 151936
-// bf16 with top-k and top-p written 247 us, against 269 us with four CTAs of
-// 256 threads (top-p draws 166 us and 165 us).  Persistent CTAs that prefetch
-// their next row to L2 were slower (242 to 293 us with more prefetched): the
-// pass over the row is bound by instruction issue, not by HBM.
+// One CTA per row.
 template <int DT, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, int groups)
 {
     using E = Elem<DT>;
     __shared__ TruncSmem<NT> sm;
-    extern __shared__ u64 list[];  // [kListCap], then the groups' maxima and sums
+    extern __shared__ u64 list[];  // [kListCap<NT>], then the groups' maxima and sums
     const int r = blockIdx.x, tid = threadIdx.x;
     for (int i = tid; i < 64; i += NT) sm.table[i] = kExp2Table[i];
     Row row = row_at<DT>(a.logits, r, a.stride, a.V);
@@ -894,7 +902,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
         sm.min_p_off = min_p_offset(st.T, a.row_min_p ? log((double)st.m) : a.log_min_p);
     // a top_k near the number of lines is found among finer groups
     const bool finer = st.k > 256 && st.k < a.V;
-    const Groups g = groups_of<DT>(row, reinterpret_cast<float*>(list + kListCap), groups, finer);
+    const Groups g = groups_of<DT>(row, reinterpret_cast<float*>(list + kListCap<NT>), groups, finer);
     // the row's whole mass matters where top_p is taken of it
     const bool sums = st.T > 0.f && st.p < 1.f && !(st.k > 0 && st.k < a.V) && a.V > kWhole;
     float m = sums ? scan_groups<DT, NT, true>(row, g, sc.ch) : scan_groups<DT, NT, false>(row, g, sc.ch);
@@ -916,7 +924,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
     List l;
     l.at = list;
     if (make_list<DT, NT>(row, g, st, sc, sums, xm, l, sm)) {
-        if (l.n <= kShort) {
+        if (l.n <= kShort<NT>) {
             u64 w;
             const int kept = short_kept<DT, NT>(row, g, st, sc, xm, l, w, sm);
             if (kept >= 0) {
@@ -950,7 +958,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
         }
     }
     bool seg_valid = false;
-    if (!sums || !band_kept<DT, NT>(row, st, sc, xm, list, sm, c, seg_valid)) {
+    if (!sums || !band_kept<DT, NT>(row, st, sc, xm, list, kListCap<NT> + groups, sm, c, seg_valid)) {
         c = find_kept<DT, NT>(row, st, sc, sm);
         seg_valid = false;
     }
@@ -971,17 +979,30 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
     }
 }
 
-template <int DT>
+template <int DT, int NT>
 cudaError_t launch(const TruncArgs& a, cudaStream_t st)
 {
-    constexpr int NT = 512;
     const int groups = groups_bound(a.V, Elem<DT>::kPerUnit);
-    const size_t smem = kListCap * sizeof(u64) + (size_t)groups * 2 * sizeof(float);
+    const size_t smem = kListCap<NT> * sizeof(u64) + (size_t)groups * 2 * sizeof(float);
     auto* kernel = truncate_kernel<DT, NT>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<a.n_rows, NT, smem, st>>>(a, groups);
     return cudaGetLastError();
+}
+
+// Few rows: CTAs of 512 threads, two on an SM, and long lists.  More rows
+// than that: four CTAs of 256 threads, whose barriers and scans cost half as
+// many instructions a row (2048 rows of 151936 bf16, top-p: 149 us against
+// 169 us; 640 x 32000 fp32 rows written: 50 us against 56 us; with
+// top-k, 2048 rows written: 241 us against 249 us).  Persistent CTAs
+// that prefetch their next row to L2 were slower (242 to 293 us in the last
+// case, with more of the row prefetched): the pass over a row is bound by instruction
+// issue, not by HBM.
+template <int DT>
+cudaError_t launch(const TruncArgs& a, cudaStream_t st)
+{
+    return a.n_rows <= 304 ? launch<DT, 512>(a, st) : launch<DT, 256>(a, st);
 }
 
 }  // namespace
