@@ -1,5 +1,6 @@
-"""Batched speculative-decoding verification on GB300 (sm_103a), and the
-draft-token sampling step before it.
+"""Batched speculative-decoding verification on GB300 (sm_103a), the
+draft-token sampling step before it (plain or truncated by top-k, top-p and
+min-p), and the distillation of a draft model from the target's top logits.
 
 A thin ctypes binding of the C-ABI in include/sdv.h (libsdv.so, built
 in-tree by ``draft_verification_row_gb300.build``).  Every step of the

@@ -188,8 +188,14 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
     const int u1 = row.n_units - (row.n_units > u0 && !whole_unit<DT>(row, row.n_units - 1) ? 1 : 0);
     const uint4* const units = reinterpret_cast<const uint4*>(row.p);
     // the student's statistics: mo the largest of its other tokens, zo their
-    // sum against mo; M the row's maximum, Z its sum against M
-    float mo, zo, Z;
+    // sum against mo; M the row's maximum, Z its sum against M, zk the part of
+    // it that the k tokens have
+    float mo, zo, Z, zk;
+    const auto token_mass = [&] {
+        float z = 0.f;
+        for (int j = tid; j < k; j += NT) z += ex2((sm.s[j] - M) * a.c);
+        return block_sum_f<NT>(z, sm.part);
+    };
     if (kStats) {
         RunningSum s = {-INFINITY, 0.f};
         for (int u = u0 + tid; u < u1; u += kUnroll * NT) {
@@ -232,9 +238,8 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
             return;
         }
         zo = block_sum_f<NT>(s.m > -INFINITY ? s.z * ex2((s.m - mo) * a.c) : 0.f, sm.part);
-        float zs = 0.f;
-        for (int j = tid; j < k; j += NT) zs += ex2((sm.s[j] - M) * a.c);
-        Z = block_sum_f<NT>(zs, sm.part) + (mo > -INFINITY ? zo * ex2((mo - M) * a.c) : 0.f);
+        zk = token_mass();
+        Z = zk + (mo > -INFINITY ? zo * ex2((mo - M) * a.c) : 0.f);
         if (stats && tid == 0) {
             stats[0] = mo;
             stats[1] = zo;
@@ -250,13 +255,19 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
             fill_row<DT, NT>(grow, NAN);
             return;
         }
+        zk = token_mass();
     }
     // the teacher's probabilities
     const bool taught = !(tm == -INFINITY);  // false: the record is empty, nothing is learnt from the row
     float zt = 0.f;
     for (int j = tid; j < k; j += NT) zt += expf(sm.p[j] - tm);
-    zt = block_sum_f<NT>(zt, sm.part) + expf(rest - tm);
-    const float lzt = logf(zt);
+    zt = block_sum_f<NT>(zt, sm.part);
+    const float all = zt + expf(rest - tm), lzt = logf(all);
+    // the k tokens' masses, 1 - p_r and 1 - q_r.  Where both are small, p_r and
+    // q_r are near 1 and have no digits left for what they differ by, which is
+    // then taken from these
+    const float P = zt / all, Q = zk / Z;
+    const bool small = P < 0.5f && Q < 0.5f;
     const float lpr = (rest - tm) - lzt, pr = expf(lpr);
     const float lz = logf(Z);
     float loss = 0.f;
@@ -267,8 +278,9 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
     }
     if (kStats) {
         loss = block_sum_f<NT>(loss, sm.part);
-        const float lo = mo > -INFINITY ? (mo - M) * a.inv_T + logf(zo) : -INFINITY;
-        if (!(pr == 0.f)) loss += pr * (lpr - (lo - lz));
+        const float lqr = mo > -INFINITY ? (mo - M) * a.inv_T + logf(zo) - lz : -INFINITY;
+        const float lr = small ? -log1pf((P - Q) / pr) : lpr - lqr;  // ln(p_r / q_r)
+        if (!(pr == 0.f)) loss += pr * lr;
         if (tid == 0) a.loss[r] = taught ? weight * loss : 0.f;
     }
     if (!kGrad) return;
@@ -279,7 +291,8 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
     const float scale = weight * (a.grad_loss ? a.grad_loss[r * a.grad_loss_stride] : 1.f) * a.inv_T;
     // another token: scale (q_i - p_r q_i / q_r), both against mo, so that
     // neither factor is lost where the k tokens hold nearly all of the mass
-    const float fo = mo > -INFINITY ? scale * (ex2((mo - M) * a.c) / Z - pr / zo) : 0.f;
+    const float fo =
+        mo > -INFINITY ? scale * (small ? (P - Q) / zo : ex2((mo - M) * a.c) / Z - pr / zo) : 0.f;
     const bool alike = grow.off == row.off;
     const float ref = mo > -INFINITY ? mo : 0.f;
     const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-ref, -ref), f2 = make_float2(fo, fo);

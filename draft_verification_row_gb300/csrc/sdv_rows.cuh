@@ -170,12 +170,15 @@ constexpr int kWeightBits = 45;
 constexpr int kWeightSpan = kWeightBits + 1;  // 2^-46 and below round to 0
 
 // The weight exp((x - M) / T) of a logit x <= M as an integer multiple of
-// 2^-45, with a relative error of about 2^-39: sums of integers do not
-// depend on their order, and 2^18 weights (the longest row) stay below 2^63.
-// A border of the kept set and a draw's crossing are then settled as 64-bit
-// arithmetic settles them, except where a sum lies within about 1e-12 of
-// them.  fp32 sums (1e-7) would move the border of a nucleus whose last
-// tokens have a mass of 1e-5 in one row of a hundred.
+// 2^-45, with a relative error of about 2^-39 before that rounding: sums of
+// integers do not depend on their order, and 2^18 weights (the longest row)
+// stay below 2^63.  A sum of n weights is off by about sqrt(n) 2^-47 of the
+// largest one (1e-12 for a whole row), at most by n 2^-46, which a row
+// reaches whose tokens nearly all lie just below 2^-46 and are dropped.  A
+// border of the kept set and a draw's crossing are then settled as 64-bit
+// arithmetic settles them, except within that distance.  fp32 sums (1e-7)
+// would move the border of a nucleus whose last tokens have a mass of 1e-5
+// in one row of a hundred.
 //   y = (x - M) c with c = log2(e) / T held in two floats; the difference
 //   and the product are exact pairs.  y = n / 64 + r with |r| <= 1/128,
 //   2^y = 2^(n >> 6) table[n & 63] (1 + (2^r - 1)), and 2^r - 1 by its

@@ -16,8 +16,9 @@
 // in shared memory.  From these follows a threshold above which all kept
 // tokens must lie; the lines that reach it are read again (from L2), their
 // tokens above it listed in index order, and everything else is done on the
-// list.  Where no short list can hold the kept set (flat rows, a large top_k,
-// no truncation), the same steps run over the row itself, from L2.
+// list.  Where no list can hold the kept set, the row is read again as a
+// whole, from L2: for top_p of flat rows twice (band_kept), else (a large
+// top_k, no truncation) once for every step.
 //
 // All masses that decide something are fixed-point integers (weight_of), so
 // every run gives the same tokens.  The mass of what is not listed is an
@@ -35,7 +36,6 @@ constexpr int kWhole = 2048;                                      // rows up to 
 // Listed tokens.
 template <int NT>
 constexpr int kListCap = NT == 512 ? 8192 : 2048;
-
 
 // Lists up to this length are ranked by counting.
 template <int NT>
@@ -344,9 +344,10 @@ __device__ __forceinline__ float light_weight(float x, const Scale& sc)
 constexpr float kOne = (float)(1ull << kWeightBits);
 
 // The bucket by which the groups' largest weights alone sum to the share p
-// of the row's mass (and each group's sum against the row's maximum): the tokens in buckets 0 to it have at least that mass,
+// of the row's mass: the tokens in buckets 0 to it have at least that mass,
 // up to the rounding of the fp32 sums.  kFar: they do not; near_miss: but
-// they hold most of it.
+// they hold most of it.  On the way every group's sum is taken against the
+// row's maximum.
 template <int NT>
 __device__ int bucket_of_share(const Groups& g, float p, const Scale& sc, TruncSmem<NT>& sm, bool& near_miss)
 {
@@ -448,8 +449,8 @@ __device__ int2 band_of_share(const Row& row, float p, const Scale& sc, TruncSme
 // the band by segments (seg), the band's tokens into the list, in any order,
 // and the rest's mass; the border is then searched in the list.  False: it
 // is not in the band, or the band is longer than room (the list, and the
-// groups behind it, which are not needed any more).  seg holds the kept mass of
-// the row's segments afterwards, unless min_p ends the kept set earlier
+// groups behind it, which are not needed any more).  seg holds the kept mass
+// of the row's segments afterwards, unless min_p ends the kept set earlier
 // (seg_valid).
 template <int DT, int NT>
 __device__ bool band_kept(const Row& row, const Settings& st, const Scale& sc, float xm, u64* list, int room,
@@ -614,8 +615,8 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
 // The mass of what is not listed, in fp32 sums (bucket_of_share has taken the
 // groups' sums against M), each weight within 2^-18 (ex2.approx 2^-22, an
 // exponent of up to 46 rounded in three places, sums of up to 64 terms), and
-// the bound on its error; or, where that leaves a
-// border open, in fixed point from the row.
+// the bound on its error; or, where that leaves a border open, in fixed point
+// from the row.
 template <int NT>
 __device__ u64 light_rest(const Groups& g, const List& l, const Scale& sc, u64& error, BlockSmem<NT>& bs)
 {
@@ -640,8 +641,7 @@ __device__ u64 exact_rest(const Row& row, const List& l, const Scale& sc, const 
     return block_sum<NT>(other, bs);
 }
 
-// The kept set from a longer list.  False: it is not within
-// the list.
+// The kept set from a longer list.  False: it is not within the list.
 template <int DT, int NT>
 __device__ bool list_kept(const Row& row, const Groups& g, const Settings& st, const Scale& sc, float xm,
                           const List& l, TruncSmem<NT>& sm, Kept& kept)

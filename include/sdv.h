@@ -33,6 +33,9 @@
  *   sdv_verify_kseq        SpecTr's K-SEQ per position, the rule whose
  *                          search for a scaling factor SpecTr-GBV avoids
  *                          (SpecTr-GBV page, sections 3-4); stated below.
+ * Around them: sdv_sample_rows and sdv_sample_truncated draw draft tokens,
+ * sdv_truncate_rows writes the truncated rows that the rules then read, and
+ * sdv_top_logits and sdv_distill_* train a draft model on the target's rows.
  *
  * The pages print none of the formulas; the rules computed are:
  *   P_v = softmax(target_row / T), Q_v = softmax(draft_row / T) at a trie
@@ -257,10 +260,10 @@ int sdv_sample_rows(int n_rows, int V, long long row_stride, int dtype, float te
  *   n_m  the tokens with w_i >= min_p (0: all).
  * The first max(1, min(n_k, n_p, n_m)) are kept; tokens whose logit is -inf
  * never are.  T = 0 keeps the row's argmax, lowest index on ties.
- * Sums are fixed-point integers with steps of 2^-45 of the largest weight:
- * the results do not depend on the order of summation, and agree with
- * 64-bit arithmetic except where a sum lies within about 1e-12 (relative)
- * of its border.
+ * Weights are rounded to multiples of 2^-45 of the largest one and summed as
+ * integers: the results do not depend on the order of summation, and agree
+ * with 64-bit arithmetic except where a sum lies within that rounding of its
+ * border (about 1e-12 of the largest weight for a whole row, at most V 2^-46).
  *   n_rows, V, dtype  as in sdv_sample_rows.
  *   row_stride   elements between rows, >= V; any value.
  *   temperature, top_k, top_p, min_p  every row's settings: T >= 0 with

@@ -153,6 +153,23 @@ def test_loss_and_gradient(dtype, V, k, T):
     _check(student, values, index, None, T)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_small_losses_keep_their_digits(dtype):
+    """Where the k tokens hold little of either mass, the loss is a small part of its terms: it is off by TOL of what
+    the k tokens hold, not of 1."""
+    teacher = _rows(6, 9576, dtype, 41)
+    student = (teacher.float() + 0.3 * torch.randn((6, 9576), generator=_gen(42), device=DEV)).to(DT[dtype])
+    for k in (1, 3):
+        values, index, rest = _record(teacher, k, 2.0)
+        loss = _check(student, values, index, rest, 2.0)
+        for r in range(6):
+            want, _ = R.distill(student[r].double().cpu().numpy(), values[r].double().cpu().numpy(),
+                                index[r].cpu().numpy(), float(rest[r]), 2.0)
+            t = np.append(values[r].double().cpu().numpy() / 2.0, float(rest[r]))
+            held = 1.0 - np.exp(t[-1] - t.max()) / np.exp(t - t.max()).sum()
+            assert held < 0.1 and abs(float(loss[r]) - want) <= TOL * held, (k, r, float(loss[r]), want)
+
+
 def test_teacher_of_another_type_and_alignment():
     teacher = _rows(4, 5003, "f32", 13)
     values, index, rest = _record(teacher, 30, 1.0)
