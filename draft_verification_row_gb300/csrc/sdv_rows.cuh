@@ -170,9 +170,9 @@ constexpr int kWeightBits = 45;
 constexpr int kWeightSpan = kWeightBits + 1;  // 2^-46 and below round to 0
 
 // The weight exp((x - M) / T) of a logit x <= M as an integer multiple of
-// 2^-45, with a relative error of about 2^-39 before that rounding: sums of
-// integers do not depend on their order, and 2^18 weights (the longest row)
-// stay below 2^63.  A sum of n weights is off by about sqrt(n) 2^-47 of the
+// 2^-45, with a relative error of up to 2^-37.7 before that rounding (rms
+// 1.3e-12, without a bias): sums of integers do not depend on their order,
+// and 2^18 weights (the longest row) stay below 2^63.  A sum of n weights is off by about sqrt(n) 2^-47 of the
 // largest one (1e-12 for a whole row), at most by n 2^-46, which a row
 // reaches whose tokens nearly all lie just below 2^-46 and are dropped.  A
 // border of the kept set and a draw's crossing are then settled as 64-bit
@@ -182,8 +182,9 @@ constexpr int kWeightSpan = kWeightBits + 1;  // 2^-46 and below round to 0
 //   y = (x - M) c with c = log2(e) / T held in two floats; the difference
 //   and the product are exact pairs.  y = n / 64 + r with |r| <= 1/128,
 //   2^y = 2^(n >> 6) table[n & 63] (1 + (2^r - 1)), and 2^r - 1 by its
-//   series, the linear term in two floats.  About 45 instructions, none of
-//   them fp64 (whose rate on this GPU is 1/64 of fp32's).
+//   series, the linear term in two floats.  About 50 instructions, none of
+//   them fp64 (whose rate on this GPU is 1/64 of fp32's) or a 64-bit
+//   conversion (with two of those, calls on flat rows took 1.15 times as long).
 struct Scale {
     float ch, cl;  // log2(e) / T = ch + cl
     float M;       // the row's maximum
@@ -193,11 +194,14 @@ __device__ __forceinline__ u64 weight_of(float x, const Scale& s, const u64* tab
 {
     const float dh = __fsub_rn(x, s.M);
     const float yh = __fmul_rn(dh, s.ch);
-    if (!(yh >= -(float)kWeightSpan)) return 0;
     const float bb = __fsub_rn(dh, x);
     const float dl = __fadd_rn(__fsub_rn(x, __fsub_rn(dh, bb)), __fsub_rn(-s.M, bb));
     const float yl = __fadd_rn(__fmaf_rn(dh, s.ch, -yh), __fmaf_rn(dh, s.cl, __fmul_rn(dl, s.ch)));
-    const float nf = rintf(yh * 64.f);
+    // a float below 2^22 plus 1.5 2^23 is its nearest integer, in the low bits
+    // too: no conversion instructions, of which an SM does few
+    constexpr float kRound = 12582912.f;
+    const float nr = __fmaf_rn(yh, 64.f, kRound), nf = __fsub_rn(nr, kRound);
+    const int n = __float_as_int(nr) - __float_as_int(kRound);
     const float r0 = __fmaf_rn(nf, -1.f / 64.f, yh);
     const float rh = __fadd_rn(r0, yl);
     const float rl = __fsub_rn(yl, __fsub_rn(rh, r0));
@@ -206,13 +210,15 @@ __device__ __forceinline__ u64 weight_of(float x, const Scale& s, const u64* tab
     float lo = __fadd_rn(__fmaf_rn(rh, kLn2, -t), __fmaf_rn(rh, kLn2Lo, __fmul_rn(rl, kLn2)));
     const float p = fmaf(rh, fmaf(rh, fmaf(rh, 0.00133335581f, 0.00961812911f), 0.0555041087f), 0.240226507f);
     lo = fmaf(rh * rh, p, lo);
-    constexpr float kUnit = 1125899906842624.f;  // 2^50
-    const long long f = __float2ll_rn(t * kUnit) + __float2ll_rn(lo * kUnit);
-    const int n = (int)nf;
+    // 2^r - 1 = t + lo in units of 2^-38, t's upper part first
+    const float tr = __fmaf_rn(t, 67108864.f, kRound), th = __fsub_rn(tr, kRound);  // 2^26
+    const float rest = __fadd_rn(lo, __fmaf_rn(th, -1.f / 67108864.f, t));
+    const float lr = __fmaf_rn(rest, 274877906944.f, kRound);  // 2^38
+    const int f = ((__float_as_int(tr) - __float_as_int(kRound)) << 12) + (__float_as_int(lr) - __float_as_int(kRound));
     const u64 e = table[n & 63];
-    const u64 w = e + (u64)__mul64hi((long long)e, f << 14);
-    const int shift = 62 - kWeightBits - (n >> 6);  // 17 .. 63
-    return (w + (1ull << (shift - 1))) >> shift;
+    const u64 w = e + (u64)((long long)f * (long long)(e >> 31) >> 7);
+    const int shift = min(max(62 - kWeightBits - (n >> 6), 17), 63);  // (17 .. 63 where it is used)
+    return yh >= -(float)kWeightSpan ? (w + (1ull << (shift - 1))) >> shift : 0;
 }
 
 // ------------------------------------------------------------------------
@@ -665,6 +671,35 @@ __device__ __forceinline__ int entry_index(u64 e) { return (int)(uint32_t)e; }
 
 constexpr int kMaxLines = (int)(sizeof(Hist) / sizeof(uint16_t));
 
+// The groups whose maximum is near, in order, into lines (in h's place);
+// returns how many there are: none are written if that is more than most.
+// All threads; ends with a barrier.
+template <int NT>
+__device__ int select_lines(const Groups& g, const Near& near, int most, uint16_t* lines, BlockSmem<NT>& bs)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    // a warp's contiguous range of the groups: how many, then which
+    const int per = (g.n + NT / 32 - 1) / (NT / 32);
+    const int g0 = min(w * per, g.n), g1 = min(g0 + per, g.n);
+    int count = 0;
+#pragma unroll 4
+    for (int i = g0 + lane; i < g1; i += 32) count += near(g.max[i]) ? 1 : 0;
+    uint32_t total;
+    int at = (int)block_scan32<NT>((uint32_t)count, total, bs);
+    at = __shfl_sync(0xffffffffu, at, 0);  // where this warp's begin
+    if (total <= (uint32_t)most) {
+#pragma unroll 4
+        for (int gb = g0; gb < g1; gb += 32) {
+            const bool mine = gb + lane < g1 && near(g.max[gb + lane]);
+            const unsigned mask = __ballot_sync(0xffffffffu, mine);
+            if (mine) lines[at + __popc(mask & ((1u << lane) - 1))] = (uint16_t)(gb + lane);
+            at += __popc(mask);
+        }
+    }
+    __syncthreads();
+    return (int)total;
+}
+
 // The logits of a row that are near (all threads), listed in index order;
 // returns how many there are, more than cap where they were not all listed,
 // and the lowest listed key.  other(raw, marks): is
@@ -677,28 +712,12 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
                        Hist& h, BlockSmem<NT>& bs, F other)
 {
     constexpr int EPU = Elem<DT>::kPerUnit, U = 4;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
     uint16_t* const lines = reinterpret_cast<uint16_t*>(&h);  // the groups to read, in order
-    // a warp's contiguous range of the groups: how many, then which
-    const int per = (g.n + NT / 32 - 1) / (NT / 32);
-    const int g0 = min(w * per, g.n), g1 = min(g0 + per, g.n);
-    int count = 0;
-#pragma unroll 4
-    for (int i = g0 + lane; i < g1; i += 32) count += near(g.max[i]) ? 1 : 0;
-    uint32_t total_lines;
-    int at = (int)block_scan32<NT>((uint32_t)count, total_lines, bs);
-    at = __shfl_sync(0xffffffffu, at, 0);  // where this warp's begin
-    const int n_lines = (int)total_lines;
     if (tid == 0) bs.low = ~0u;
-    if (n_lines > cap || n_lines > kMaxLines) return cap + 1;  // each has a near logit at least
-#pragma unroll 4
-    for (int gb = g0; gb < g1; gb += 32) {
-        const bool mine = gb + lane < g1 && near(g.max[gb + lane]);
-        const unsigned mask = __ballot_sync(0xffffffffu, mine);
-        if (mine) lines[at + __popc(mask & ((1u << lane) - 1))] = (uint16_t)(gb + lane);
-        at += __popc(mask);
-    }
-    __syncthreads();
+    const int most = min(cap, kMaxLines);  // each has a near logit at least
+    const int n_lines = select_lines<NT>(g, near, most, lines, bs);
+    if (n_lines > most) return cap + 1;
     const int n_units = n_lines << g.shift, in_group = (1 << g.shift) - 1;
     int n = 0;
     uint32_t low = ~0u;

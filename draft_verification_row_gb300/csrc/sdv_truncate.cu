@@ -334,11 +334,17 @@ __device__ Kept find_kept(const Row& row, const Settings& st, const Scale& sc, T
     return kept;
 }
 
-// The weight exp((x - M) / T) in fp32 (nothing of it is left below 2^-126).
+// The weight exp((x - M) / T) in fp32, within 2^-21 (ex2.approx 2^-22; the
+// exponent's rounding is made up for; nothing is left below 2^-126).
 __device__ __forceinline__ float light_weight(float x, const Scale& sc)
 {
-    const float d = x - sc.M;
-    return d * sc.ch >= -130.f ? ex2(fmaf(d, sc.ch, d * sc.cl)) : 0.f;
+    const float d = __fsub_rn(x, sc.M), y = __fmul_rn(d, sc.ch);
+    if (!(y >= -130.f)) return 0.f;
+    const float bb = __fsub_rn(d, x);
+    const float dl = __fadd_rn(__fsub_rn(x, __fsub_rn(d, bb)), __fsub_rn(-sc.M, bb));
+    const float left = __fmaf_rn(d, sc.ch, -y) + fmaf(d, sc.cl, dl * sc.ch);
+    const float w = ex2(y);
+    return fmaf(w, left * 0.693147182f, w);
 }
 
 constexpr float kOne = (float)(1ull << kWeightBits);
@@ -612,33 +618,79 @@ __device__ bool make_list(const Row& row, const Groups& g, const Settings& st, c
     return l.n <= kListCap<NT>;
 }
 
-// The mass of what is not listed, in fp32 sums (bucket_of_share has taken the
-// groups' sums against M), each weight within 2^-18 (ex2.approx 2^-22, an
-// exponent of up to 46 rounded in three places, sums of up to 64 terms), and
-// the bound on its error; or, where that leaves a border open, in fixed point
-// from the row.
-template <int NT>
-__device__ u64 light_rest(const Groups& g, const List& l, const Scale& sc, u64& error, BlockSmem<NT>& bs)
-{
-    float rest = l.rest;
-    const Near near(sc.M, l.top);
-    for (int i = threadIdx.x; i < g.n; i += NT)
-        if (!near(g.max[i])) rest += g.sum[i];
-    const u64 other = block_sum<NT>((u64)(rest * kOne), bs);
-    error = (other >> 18) + 64 * NT;
-    return other;
-}
-
+// The mass of what is not listed, and the bound on its error.  Step 0: from
+// fp32 sums.  A group's sum (bucket_of_share has taken it against M) is
+// within 2^-19: in units of 2^-24, 5 from the exponents within the group
+// (whose mean, weighted, is below 3.4 in any group of 64), 4 from ex2.approx,
+// 8 from its additions and 9 from light_weight and the product.  What the
+// lines read again have beside listed tokens has exponents of up to 46, each
+// rounded twice: within 2^-17.  (The largest deviation met in 140000 rows was
+// 2^-21.2.)  That leaves the border open in a row of a thousand or two (2048
+// x 151936 bf16, top-p 0.9), which is then read again: step 1 sums weights
+// above 2^-20 in fixed point, which are a small part of the row (they are
+// brought together in shared memory first, so that all lanes have work), and
+// the others in fp32; step 2 sums all in fixed point.
 template <int DT, int NT>
-__device__ u64 exact_rest(const Row& row, const List& l, const Scale& sc, const u64* table, BlockSmem<NT>& bs)
+__device__ u64 rest_mass(const Row& row, const Groups& g, const List& l, const Scale& sc, int step, u64& error,
+                         TruncSmem<NT>& sm)
 {
-    u64 other = 0;
-    const RowSource<DT, NT> all{row};
-    const Near near(sc.M, l.top);
-    all.each([&](float x) {
-        if (!near(x)) other += weight_of(x, sc, table);
-    });
-    return block_sum<NT>(other, bs);
+    constexpr int EPU = Elem<DT>::kPerUnit, U = 4, kRoom = 2 * kBuckets;
+    const int tid = threadIdx.x;
+    const Near listed(sc.M, l.top);
+    if (step == 0) {
+        u64 lines = 0;
+        for (int i = tid; i < g.n; i += NT)
+            if (!listed(g.max[i])) lines += (u64)(g.sum[i] * kOne);
+        lines = block_sum<NT>(lines, sm.bs);
+        const u64 rest = block_sum<NT>((u64)(l.rest * kOne), sm.bs);
+        error = (lines >> 19) + (rest >> 17) + 64 * NT;
+        return lines + rest;
+    }
+    float* const heavy = reinterpret_cast<float*>(&sm.hist);
+    const float from = step == 1 ? sc.M - 20.f / sc.ch : -INFINITY;  // weights in fixed point
+    u64 exact = 0;
+    float light = 0.f;
+    __syncthreads();
+    if (tid == 0) sm.count = 0;
+    __syncthreads();
+    for (int u0 = tid; u0 - tid < row.n_units; u0 += U * NT) {
+        uint4 raw[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) raw[i] = load_unit_or_none<DT>(row, u0 + i * NT);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float v[EPU];
+            Elem<DT>::unpack(raw[i], v);
+            uint32_t mine = 0, gone = 0;
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) {
+                const bool in = listed(v[e]);
+                mine |= (!in && v[e] > from ? 1u : 0u) << e;
+                gone |= (in ? 1u : 0u) << e;
+            }
+            light += unit_sum<DT>(without<DT>(raw[i], mine | gone), sc.ch, sc.M);
+            if (!mine) continue;
+            int at = atomicAdd(&sm.count, __popc(mine));
+#pragma unroll
+            for (int e = 0; e < EPU; ++e) {
+                if (!(mine >> e & 1)) continue;
+                if (at < kRoom)
+                    heavy[at] = v[e];
+                else
+                    exact += weight_of(v[e], sc, sm.table);
+                ++at;
+            }
+        }
+        __syncthreads();
+        const int n = min(sm.count, kRoom);
+        for (int i = tid; i < n; i += NT) exact += weight_of(heavy[i], sc, sm.table);
+        __syncthreads();
+        if (tid == 0) sm.count = 0;
+        __syncthreads();
+    }
+    const u64 other = block_sum<NT>((u64)(light * kOne), sm.bs);
+    error = step == 1 ? (other >> 17) + 64 * NT : 0;
+    return other + block_sum<NT>(exact, sm.bs);
 }
 
 // The kept set from a longer list.  False: it is not within the list.
@@ -663,8 +715,8 @@ __device__ bool list_kept(const Row& row, const Groups& g, const Settings& st, c
             u64 listed = 0, error;
             src.each([&](float x) { listed += weight_of(x, sc, sm.table); });
             listed = block_sum<NT>(listed, sm.bs);
-            u64 other = light_rest<NT>(g, l, sc, error, sm.bs);
-            for (;;) {
+            for (int step = 0;; ++step) {
+                const u64 other = rest_mass<DT, NT>(row, g, l, sc, step, error, sm);
                 const u64 lo = share_of(st.p, listed + (other > error ? other - error : 0));
                 const u64 hi = share_of(st.p, listed + other + error);
                 if (listed < lo) {  // the border lies below the list, which min_p ends or no one knows
@@ -679,8 +731,6 @@ __device__ bool list_kept(const Row& row, const Groups& g, const Settings& st, c
                     c.ties = ties;
                     break;
                 }
-                other = exact_rest<DT, NT>(row, l, sc, sm.table, sm.bs);
-                error = 0;
             }
         }
         if (xm > -INFINITY) cut_at_logit<DT>(xm, c);
@@ -732,8 +782,8 @@ __device__ int short_kept(const Row& row, const Groups& g, const Settings& st, c
         u64 listed;
         const u64 before = block_scan<NT>(tid < limit ? sorted[tid] : 0, listed, sm.bs);
         u64 other = 0, error = 0;
-        if (!by_count && !l.whole) other = light_rest<NT>(g, l, sc, error, sm.bs);
-        for (;;) {
+        for (int step = 0;; ++step) {
+            if (!by_count && !l.whole) other = rest_mass<DT, NT>(row, g, l, sc, step, error, sm);
             const u64 lo = share_of(st.p, listed + (other > error ? other - error : 0));
             if (listed < lo) {  // the border lies below the list, which min_p ends or no one knows
                 if (!l.ends) return -1;
@@ -743,8 +793,6 @@ __device__ int short_kept(const Row& row, const Groups& g, const Settings& st, c
             if (error == 0) break;
             const u64 hi = share_of(st.p, listed + other + error);
             if (hi <= listed && n == __syncthreads_count(tid < limit && before < hi)) break;
-            other = exact_rest<DT, NT>(row, l, sc, sm.table, sm.bs);
-            error = 0;
         }
     }
     return mine && rank < n && x >= xm;
@@ -991,18 +1039,25 @@ cudaError_t launch(const TruncArgs& a, cudaStream_t st)
     return cudaGetLastError();
 }
 
-// Few rows: CTAs of 512 threads, two on an SM, and long lists.  More rows
-// than that: four CTAs of 256 threads, whose barriers and scans cost half as
-// many instructions a row (2048 rows of 151936 bf16, top-p: 149 us against
-// 169 us; 640 x 32000 fp32 rows written: 50 us against 56 us; with
-// top-k, 2048 rows written: 241 us against 249 us).  Persistent CTAs
-// that prefetch their next row to L2 were slower (242 to 293 us in the last
-// case, with more of the row prefetched): the pass over a row is bound by instruction
-// issue, not by HBM.
+// CTAs of 512 threads, two on an SM, with lists of 8192 tokens; or four of
+// 256, whose barriers and scans cost half as many instructions a row, with
+// lists of 2048.  The small ones take calls of more rows than fit at once (640
+// x 32000 fp32 rows, top-p and min-p written: 50 us against 56 us; 2048 x
+// 151936 bf16, top-k and top-p written: 241 us against 249 us), but not
+// top_p of long rows' whole mass: among those some rows are flatter than 2048
+// tokens, or have to be summed again, and one of them in a small CTA at the
+// end makes the call wait (2048 x 151936 bf16, top-p 0.9 drawn, eight seeds:
+// 151 to 354 us, 203 in the mean, against 170 to 222 us, 186 in the mean; T
+// 0.8, normal rows: 477 us against 270 us for 512 rows).  Persistent CTAs that
+// prefetch their next row to L2 were slower (242 to 293 us in the second case,
+// with more of the row prefetched): the pass over a row is bound by
+// instruction issue, not by HBM.
 template <int DT>
 cudaError_t launch(const TruncArgs& a, cudaStream_t st)
 {
-    return a.n_rows <= 304 ? launch<DT, 512>(a, st) : launch<DT, 256>(a, st);
+    const bool whole_mass = (a.row_top_p || a.top_p < 1.f) && (a.row_top_k || a.top_k == 0 || a.top_k >= a.V);
+    if (a.n_rows <= 304 || (whole_mass && a.V > 65536)) return launch<DT, 512>(a, st);
+    return launch<DT, 256>(a, st);
 }
 
 }  // namespace

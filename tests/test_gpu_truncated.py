@@ -104,6 +104,28 @@ def test_wide_kept_sets(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,head,tail", [(5003, 0.0, -10.0), (40007, 0.0, -11.0), (5003, -4.0, -5.0),
+                                         (40007, -4.0, -5.5), (151936, -8.0, -10.0), (151936, 0.0, -12.0)])
+def test_borders_that_fp32_sums_leave_open(dtype, V, head, tail):
+    """top_p is the fp32 number just below, at and above the share of the tokens up to a border: p Z and the sum there
+    differ by 1e-8 to 1e-7 of Z, less than the error of the fp32 mass of the tail."""
+    g = _gen(V)
+    x = torch.full((3, V), tail, device=DEV)
+    where = torch.randperm(V, generator=g, device=DEV)
+    x[:, where[:1]] = 0.0
+    x[:, where[1:41]] = head
+    x += (torch.rand((3, V), generator=g, device=DEV) < 0.5) * 0.125 * (x == tail)  # two levels of the tail
+    x = x.to(DT[dtype])
+    for r in range(3):
+        w = torch.exp(x[r].double()).sort(descending=True).values
+        share = (w.cumsum(0) / w.sum())[[0, 20, 40][r]].item()
+        p = np.float32(share)
+        for q in (np.nextafter(p, np.float32(0)), p, np.nextafter(p, np.float32(1))):
+            _check(x[r:r + 1], 1.0, p=float(q))
+            _check(x, 1.0, p=float(q), m=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [3072, 3073, 8191, 50021, 151936])
 def test_flat_rows(dtype, V):
     """Kept sets from a few hundred tokens to most of the row, where lists end and whole-row passes begin."""
