@@ -88,7 +88,7 @@ __device__ __forceinline__ void store_unit(const Row& g, bool alike, const Row& 
         else
             w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4 % EPU], v[5 % EPU]),
                            pack_bf16(v[6 % EPU], v[7 % EPU]));
-        reinterpret_cast<uint4*>(g.p)[u] = w;
+        __stcs(reinterpret_cast<uint4*>(g.p) + u, w);  // not read again: L2 keeps the rows
         return;
     }
 #pragma unroll
@@ -308,18 +308,22 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
         }
         store_unit<DT>(grow, alike, row, u, v);
     };
+    // a thread's own units of the first pass, the last ones first: they are the
+    // likeliest to be in L2 still
     const int cached = kStats ? min(a.cached, u1) : 0;
-    for (int u = u0 + tid; u < cached; u += NT) put(u, cache[u]);  // a thread's own units
-    int u = u0 + tid;
-    if (u < cached) u += (cached - u + NT - 1) / NT * NT;
-    for (; u < u1; u += kUnroll * NT) {
-        uint4 raw[kUnroll];
+    int first = u0 + tid;
+    if (first < cached) first += (cached - first + NT - 1) / NT * NT;
+    if (first < u1) {
+        for (int u = first + (u1 - 1 - first) / NT * NT; u >= first; u -= kUnroll * NT) {
+            uint4 raw[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) raw[i] = u + i * NT < u1 ? units[u + i * NT] : no_unit<DT>();
+            for (int i = 0; i < kUnroll; ++i) raw[i] = u - i * NT >= first ? __ldcs(units + u - i * NT) : no_unit<DT>();
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-            if (u + i * NT < u1) put(u + i * NT, raw[i]);
+            for (int i = 0; i < kUnroll; ++i)
+                if (u - i * NT >= first) put(u - i * NT, raw[i]);
+        }
     }
+    for (int u = u0 + tid; u < cached; u += NT) put(u, cache[u]);
     if (tid == 0 && u0 > 0) put(0, edge_unit<DT>(row, 0));
     if (tid == 1 && u1 < row.n_units) put(row.n_units - 1, edge_unit<DT>(row, row.n_units - 1));
     __syncthreads();  // the teacher's tokens are written over
@@ -349,13 +353,16 @@ cudaError_t launch(DistillArgs a, bool cache, cudaStream_t st)
     return cudaGetLastError();
 }
 
-// CTA shapes (8192 rows of 151936 bf16 unless stated).  Loss and gradient:
-// the second pass finds the row in L2 only while few rows are in flight.
-// Long rows: 304 CTAs of 512 threads, 48 KB of each row kept in shared
-// memory: 942 us; 456 CTAs 1090 us, 912 CTAs of 256 threads 1049 us (with
-// 96 KB kept, 1142 us).  Rows of up to 96 KB: many small CTAs, whose fixed
-// work per row overlaps better: 1000 x 20011 fp32 41 us against 48 us.  The
-// loss alone, 512 x 128256 bf16: 31 us against 35 us.
+// CTA shapes.  Loss and gradient: the second pass finds the row in L2 only
+// while few rows are in flight.  Long rows (8192 x 151936 bf16): 304 CTAs of
+// 512 threads, 48 KB of each row kept in shared memory, the rest read again
+// from its end and streamed, the gradient streamed out: 864 us, 0.85 of the
+// copy rate (883 us without streaming loads, 942 us from the row's start with
+// plain stores, 915 us with nothing kept; 456 CTAs 1050 us, 608 CTAs of 256
+// threads 1214 us).  Rows of up to 96 KB: many small CTAs, whose fixed work per
+// row overlaps better: 1000 x 20011 fp32 35 us, against 41 us with four units
+// in flight in fewer.  The loss alone, 512 x 128256 bf16: 28 us, against 35 us
+// in CTAs of 512 threads.
 template <int DT, int MODE>
 cudaError_t launch(const DistillArgs& a, cudaStream_t st)
 {
