@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
     if (tid == 0) sm.bad = 0;
     __syncthreads();
     const float rest = a.rest ? a.rest[r] : -INFINITY;
-    float tm = rest;  // already divided by T, as every teacher value below
+    float tm = -INFINITY;  // the record's largest value
     float M = -INFINITY;
     for (int j = tid; j < k; j += NT) {
         const size_t o = (size_t)r * k + j;
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
         float t = a.teacher_dtype == SDV_F32
                       ? static_cast<const float*>(a.values)[o]
                       : __uint_as_float((uint32_t) static_cast<const unsigned short*>(a.values)[o] << 16);
-        t = x < 0 ? -INFINITY : t * a.inv_T;
+        t = x < 0 ? -INFINITY : t;
         float s = -INFINITY;
         if (x >= a.V) {
             atomicOr(&sm.bad, SDV_REQ_BAD_TOKEN);
@@ -257,22 +257,34 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
         }
         zk = token_mass();
     }
-    // the teacher's probabilities
-    const bool taught = !(tm == -INFINITY);  // false: the record is empty, nothing is learnt from the row
+    // the teacher's probabilities: exponents t of its values and tr of rest
+    // (which is in units of T already) against the largest of them; values
+    // are subtracted before they are divided by T, since the lowest finite
+    // ones, which masks write, may not be representable afterwards
+    const bool taught = !(tm == -INFINITY && rest == -INFINITY);  // false: nothing is learnt from the row
+    const float ref = tm > -INFINITY ? tm : 0.f;
+    // +inf: the values are nothing beside rest
+    const float above = rest == -INFINITY ? rest : rest - ref * a.inv_T;
+    const float top = tm == -INFINITY ? above : fmaxf(above, 0.f);
+    const float tr = above == INFINITY ? 0.f : above - top, er = expf(tr);
     float zt = 0.f;
-    for (int j = tid; j < k; j += NT) zt += expf(sm.p[j] - tm);
+    for (int j = tid; j < k; j += NT) {
+        const float t = (sm.p[j] - ref) * a.inv_T - top;
+        sm.p[j] = t;
+        zt += expf(t);
+    }
     zt = block_sum_f<NT>(zt, sm.part);
-    const float all = zt + expf(rest - tm), lzt = logf(all);
+    const float all = zt + er, lzt = logf(all);
     // the k tokens' masses, 1 - p_r and 1 - q_r.  Where both are small, p_r and
     // q_r are near 1 and have no digits left for what they differ by, which is
     // then taken from these
     const float P = zt / all, Q = zk / Z;
     const bool small = P < 0.5f && Q < 0.5f;
-    const float lpr = (rest - tm) - lzt, pr = expf(lpr);
+    const float lpr = tr - lzt, pr = expf(lpr);
     const float lz = logf(Z);
     float loss = 0.f;
     for (int j = tid; j < k; j += NT) {
-        const float lp = (sm.p[j] - tm) - lzt, p = expf(lp);
+        const float lp = sm.p[j] - lzt, p = expf(lp);
         if (kStats && !(p == 0.f)) loss += p * (lp - ((sm.s[j] - M) * a.inv_T - lz));
         sm.p[j] = p;
     }
@@ -294,8 +306,8 @@ __global__ void __launch_bounds__(NT, PER_SM) distill_kernel(DistillArgs a)
     const float fo =
         mo > -INFINITY ? scale * (small ? (P - Q) / zo : ex2((mo - M) * a.c) / Z - pr / zo) : 0.f;
     const bool alike = grow.off == row.off;
-    const float ref = mo > -INFINITY ? mo : 0.f;
-    const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-ref, -ref), f2 = make_float2(fo, fo);
+    const float base = mo > -INFINITY ? mo : 0.f;
+    const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-base, -base), f2 = make_float2(fo, fo);
     const auto put = [&](int u, const uint4& raw) {
         float v[EPU];
         E::unpack(raw, v);

@@ -50,7 +50,7 @@ struct TruncSmem {
     int last;          // index of the last kept token of the border's key
     int count;         // band_kept: the band's tokens
     int2 band;
-    float2 min_p_off;  // T ln(min_p)
+    double min_p_off;  // T ln(min_p)
     uint4 edge[2];
 };
 
@@ -270,24 +270,9 @@ __device__ void cut_at_share(const Src& src, float p, uint32_t kmax, const Scale
     }
 }
 
-// The lowest fp32 number that min_p may keep, M + T ln(min_p) rounded up;
-// the second term is in two floats.
-__device__ __forceinline__ float min_p_logit(float M, float2 off)
-{
-    const float s = __fadd_rn(M, off.x);
-    const float bb = __fsub_rn(s, M);
-    const float left = __fadd_rn(__fadd_rn(__fsub_rn(M, __fsub_rn(s, bb)), __fsub_rn(off.x, bb)), off.y);
-    if (!(left > 0.f)) return s;
-    return s >= 0.f ? __uint_as_float(__float_as_uint(s) + 1) : -__uint_as_float(__float_as_uint(-s) - 1);
-}
-
-// T ln(min_p) in two floats (one thread: fp64).
-__device__ __forceinline__ float2 min_p_offset(float T, double log_min_p)
-{
-    const double d = (double)T * log_min_p;
-    const float hi = (float)d;
-    return make_float2(hi, (float)(d - (double)hi));
-}
+// The lowest fp32 number that min_p keeps, M + T ln(min_p) rounded up (off:
+// the second term).  In fp64, since a logit may lie within 1e-13 of it.
+__device__ __forceinline__ float min_p_logit(float M, double off) { return __double2float_ru((double)M + off); }
 
 template <int DT>
 __device__ __forceinline__ void cut_at_logit(float x, Cut& c)
@@ -947,7 +932,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) truncate_kernel(TruncArgs a, in
     Scale sc;
     set_scale(sc, st.ok ? st.T : 0.f);
     if (tid == 0 && st.ok && st.m > 0.f)
-        sm.min_p_off = min_p_offset(st.T, a.row_min_p ? log((double)st.m) : a.log_min_p);
+        sm.min_p_off = (double)st.T * (a.row_min_p ? log((double)st.m) : a.log_min_p);
     // a top_k near the number of lines is found among finer groups
     const bool finer = st.k > 256 && st.k < a.V;
     const Groups g = groups_of<DT>(row, reinterpret_cast<float*>(list + kListCap<NT>), groups, finer);

@@ -219,6 +219,12 @@ def test_extreme_rows(dtype):
     low[1, 30:] = torch.finfo(DT[dtype]).min
     _check(low, values, index, rest, 1.0)
     _check(low, values, index, None, 2.0)
+    masked = torch.full_like(teacher, torch.finfo(DT[dtype]).min)  # teachers whose listed logits are masks, too
+    masked[:3, 5] = 1.0
+    mv, mi, mr = _record(masked, 4, 1.0)
+    small = s.float().clamp(min=-50.0).to(DT[dtype])
+    _check(small, mv, mi, None, 0.5)
+    _check(small, mv, mi, torch.zeros(5, device=DEV), 0.5)
     s[4, int(index[4, 0])] = float("-inf")  # a token the teacher wants and the student rules out
     loss = _check(s, values, index, rest, 1.0)
     assert float(loss[4]) == float("inf")
