@@ -126,7 +126,7 @@ def test_borders_that_fp32_sums_leave_open(dtype, V, head, tail):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("V", [3072, 3073, 8191, 50021, 151936])
+@pytest.mark.parametrize("V", [2048, 2049, 8191, 50021, 151936])
 def test_flat_rows(dtype, V):
     """Kept sets from a few hundred tokens to most of the row, where lists end and whole-row passes begin."""
     for std, T, p in ((3.0, 1.0, 0.9), (2.0, 1.0, 0.9), (3.0, 1.2, 0.95), (2.0, 0.6, 0.8), (1.0, 1.0, 0.99)):
