@@ -696,27 +696,27 @@ __device__ int select_lines(const Groups& g, const Near& near, int most, uint16_
 }
 
 // The logits of a row that are near (all threads), listed in index order;
-// returns how many there are, more than cap where they were not all listed,
-// and the lowest listed key.  other(raw, marks): is
-// called for each unit of the lines read, with the marks of its listed
-// elements.  The lines' loads are all in flight together, so this waits for
-// L2 once (per 4 NT units); sums over four units a thread go through one
-// scan, 16 bits each.  Ends with a barrier.
+// returns how many there are, more than cap where there is no list (they are
+// more than that, or in more than max_lines groups), and the lowest listed
+// key.  other(raw, marks): is called for each unit of the lines read, with
+// the marks of its listed elements.  The lines' loads are all in flight
+// together, so this waits for L2 once (per 4 NT units); sums over four units
+// a thread go through one scan, 16 bits each.  Ends with a barrier.
 template <int DT, int NT, class F>
-__device__ int collect(const Row& row, const Groups& g, const Near& near, u64* list, int cap, uint32_t& lowest,
-                       Hist& h, BlockSmem<NT>& bs, F other)
+__device__ int collect(const Row& row, const Groups& g, const Near& near, int max_lines, u64* list, int cap,
+                       uint32_t& lowest, Hist& h, BlockSmem<NT>& bs, F other)
 {
     constexpr int EPU = Elem<DT>::kPerUnit, U = 4;
     const int tid = threadIdx.x, lane = tid & 31;
     uint16_t* const lines = reinterpret_cast<uint16_t*>(&h);  // the groups to read, in order
     if (tid == 0) bs.low = ~0u;
-    const int most = min(cap, kMaxLines);  // each has a near logit at least
+    const int most = min(max_lines, min(cap, kMaxLines));  // each has a near logit at least
     const int n_lines = select_lines<NT>(g, near, most, lines, bs);
     if (n_lines > most) return cap + 1;
     const int n_units = n_lines << g.shift, in_group = (1 << g.shift) - 1;
     int n = 0;
     uint32_t low = ~0u;
-    for (int p0 = 0; p0 < n_units && n <= cap; p0 += U * NT) {
+    for (int p0 = 0; p0 < n_units; p0 += U * NT) {
         uint4 raw[U];
         int unit[U];
 #pragma unroll
@@ -750,6 +750,7 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
             first[i] = n + (int)(before >> (16 * i) & 0xffffu);
             n += (int)(total >> (16 * i) & 0xffffu);
         }
+        if (n > cap) break;
         while (marks) {
             const int b = __ffs(marks) - 1, i = b >> 3;
             marks &= marks - 1;
@@ -758,8 +759,7 @@ __device__ int collect(const Row& row, const Groups& g, const Near& near, u64* l
             const int x = u * EPU + (b & 7) - row.off;
             const uint32_t k = key_of<DT>(load_elem<DT>(row, x));
             low = min(low, k);
-            if (to < cap) list[to] = list_entry(k, x);
-            ++to;
+            list[to++] = list_entry(k, x);
         }
     }
     low = __reduce_min_sync(0xffffffffu, low);

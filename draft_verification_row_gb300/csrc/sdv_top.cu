@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) top_kernel(TopArgs a, int group
     int n = kTopList + 1;  // candidates, then listed tokens
     uint32_t low = 0;
     if (whole || top < kFar)
-        n = collect<DT, NT>(row, g, Near(M, top), cand, kTopList, low, sm.hist, sm.bs,
+        n = collect<DT, NT>(row, g, Near(M, top), g.n, cand, kTopList, low, sm.hist, sm.bs,
                             [&](const uint4& raw, uint32_t marks) {
                                 const uint4 left = without<DT>(raw, marks);
                                 const float m = E::unit_max(left, -INFINITY);

@@ -137,6 +137,19 @@ def test_flat_rows(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,V", [(2, 2049), (2, 40007), (310, 5003), (2, 151936)])
+def test_mostly_masked_rows(dtype, n, V):
+    """Rows with few tokens left, fewer than top_k among them, spread over the row or side by side."""
+    for left in (1, 3, 60, 1000, 1500):
+        x = _rows(n, V, dtype, 71 + V + left)
+        place = torch.rand((n, V), generator=_gen(72), device=DEV).argsort(1)
+        place[0] = (torch.arange(V, device=DEV) + V // 3) % V
+        x.scatter_(1, place[:, left:], float("-inf"))
+        for kw in ({"k": 50}, {"k": 1200, "p": 0.9}, {"p": 0.95}, {"k": 2000, "m": 1e-4}, {"m": 1e-30}):
+            _check(x, 0.8, draws=3, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [1000, 40007])
 def test_ties(dtype, V):
     """Few distinct values: borders inside ties go by index."""
