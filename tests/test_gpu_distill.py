@@ -85,6 +85,19 @@ def test_top_logits_ties_masks_alignment(dtype):
     _check_top(peaked, 1, 1.0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [4097, 40007, 151936])
+def test_top_logits_of_mostly_masked_rows(dtype, V):
+    """Few tokens left, spread over the row or side by side, fewer and more than k."""
+    for left in (1, 3, 60, 1000, 1500):
+        x = _rows(2, V, dtype, 75 + V + left)
+        place = torch.rand((2, V), generator=_gen(76), device=DEV).argsort(1)
+        place[0] = (torch.arange(V, device=DEV) + V // 3) % V
+        x.scatter_(1, place[:, left:], float("-inf"))
+        for k in (1, 50, 1024):
+            _check_top(x, k, 0.8)
+
+
 def test_top_logits_unusable_rows():
     x = _rows(4, 3000, "bf16", 9)
     x[1, 5] = float("nan")
